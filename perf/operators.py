@@ -307,9 +307,8 @@ def nearest(grid, x):
 
 
 def all_scales(device):
-    b = torch.arange(227, dtype=torch.float64, device=device)
-    e = torch.floor(b / 8)
-    return torch.where(b < 8, b * 2.0**-17, (1 + (b - 8 * e) / 8) * torch.pow(torch.tensor(2.0, dtype=torch.float64, device=device), e - 15))
+    values = [b * 2.0**-17 if b < 8 else (1 + b % 8 / 8) * 2.0 ** (b // 8 - 15) for b in range(227)]
+    return torch.tensor(values, dtype=torch.float64, device=device)
 
 
 def exact_rounded(x):
