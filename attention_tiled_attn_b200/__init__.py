@@ -8,8 +8,10 @@ no CPU fallback: without the built library or a CUDA device the calls raise.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -57,6 +59,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.attn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, cf, ci, vp, ci, ci, ci,
                              vp, vp, vp, vp]
     lib.attn_bwd.restype = ci
+    cz = ctypes.c_size_t
+    lib.attn_kv4_write.argtypes = [vp] * 6 + [ci] * 6 + [cz] * 6 + [ci, vp, vp, ci, vp]
+    lib.attn_kv4_write.restype = ci
+    lib.attn_kv4_read.argtypes = [vp] * 6 + [ci] * 6 + [ci, vp, vp, ci, vp]
+    lib.attn_kv4_read.restype = ci
+    lib.attn_decode_kv4.argtypes = [vp] * 7 + [ci] * 8 + [cf, ci, vp, ci, ci, ci, vp, vp, cz, vp]
+    lib.attn_decode_kv4.restype = ci
+    lib.attn_decode_kv4_workspace_bytes.argtypes = []
+    lib.attn_decode_kv4_workspace_bytes.restype = cz
     lib.attn_status_string.argtypes = [ci]
     lib.attn_status_string.restype = ctypes.c_char_p
     lib.attn_release_workspace.argtypes = []
@@ -338,6 +349,245 @@ def attn_decode_indexed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_i
     return out, lse
 
 
+class KV4Cache(NamedTuple):
+    """A key/value cache in 4 bits: uint8 CUDA tensors, contiguous, `capacity` rows of every (batch, KV head).
+
+    k_codes (N, H, capacity, E/2), k_scales (N, H, capacity, E/16), v_codes
+    (N, H, capacity, Ev/2), v_scales (N, H, capacity, Ev/16); the format is
+    described in include/attn_b200.h.  A plain tuple of the four does as well.
+    """
+
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def kv4_cache(N: int, H: int, capacity: int, E: int, Ev: int | None = None, device="cuda") -> KV4Cache:
+    """An empty 4-bit cache (all rows 0).  capacity is rounded up to a multiple of 16."""
+    Ev = E if Ev is None else Ev
+    C = -(-int(capacity) // 16) * 16
+    return KV4Cache(*(torch.zeros((N, H, C, w), dtype=torch.uint8, device=device)
+                      for w in (E // 2, E // 16, Ev // 2, Ev // 16)))
+
+
+def _cache_shape(cache):
+    """Checks a 4-bit cache's tensors and returns (N, H, capacity, E, Ev)."""
+    kc, ks, vc, vs = cache
+    N, H, C, half = kc.shape
+    half_v = vc.shape[3]
+    lead = (N, H, C)
+    if (tuple(ks.shape) != lead + (half // 8,) or tuple(vc.shape) != lead + (half_v,)
+            or tuple(vs.shape) != lead + (half_v // 8,)):
+        raise ValueError("the cache's tensors must be (N, H, C, E/2), (N, H, C, E/16), (N, H, C, Ev/2), (N, H, C, Ev/16)")
+    dev = kc.device
+    for t in (kc, ks, vc, vs):
+        if t.dtype != torch.uint8 or not t.is_cuda or t.device != dev or not t.is_contiguous():
+            raise ValueError("the cache must be contiguous uint8 CUDA tensors on one device")
+    return N, H, C, 2 * half, 2 * half_v
+
+
+def _check_index(name: str, t, N: int, device):
+    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != N or t.device != device
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape ({N},) on {device}")
+
+
+def _int32(name: str, x) -> int:
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} must fit in 32 bits")
+    return x
+
+
+def _on(device, stream):
+    """Makes `device` and `stream` (None: the device's current stream) the current ones, so that what the call
+    allocates belongs to the stream it is used on."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _same_stream_device(stream, device):
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, not on {device} with the tensors")
+
+
+def attn_kv4_write_raw(k_ptr, v_ptr, kc_ptr, ks_ptr, vc_ptr, vs_ptr, N, H, L, C, E, Ev, k_strides, v_strides, start,
+                       pos_ptr, count_ptr, dtype, stream_ptr) -> int:
+    """The cache-writing C entry point with integer pointers; returns the status code."""
+    lib = load_library()
+    c = lambda p: None if p is None else ctypes.c_void_p(int(p))  # noqa: E731
+    return lib.attn_kv4_write(c(k_ptr), c(v_ptr), c(kc_ptr), c(ks_ptr), c(vc_ptr), c(vs_ptr), int(N), int(H), int(L),
+                              int(C), int(E), int(Ev), *map(int, k_strides), *map(int, v_strides), int(start),
+                              c(pos_ptr), c(count_ptr), int(dtype), c(stream_ptr))
+
+
+def attn_kv4_read_raw(kc_ptr, ks_ptr, vc_ptr, vs_ptr, k_ptr, v_ptr, N, H, rows, C, E, Ev, start, pos_ptr, len_ptr,
+                      dtype, stream_ptr) -> int:
+    """The cache-reading C entry point with integer pointers; returns the status code."""
+    lib = load_library()
+    c = lambda p: None if p is None else ctypes.c_void_p(int(p))  # noqa: E731
+    return lib.attn_kv4_read(c(kc_ptr), c(ks_ptr), c(vc_ptr), c(vs_ptr), c(k_ptr), c(v_ptr), int(N), int(H), int(rows),
+                             int(C), int(E), int(Ev), int(start), c(pos_ptr), c(len_ptr), int(dtype), c(stream_ptr))
+
+
+def attn_decode_kv4_raw(q_ptr, kc_ptr, ks_ptr, vc_ptr, vs_ptr, out_ptr, lse_ptr, N, Hq, H, L, S, C, E, Ev, scale, mode,
+                        sink_ptr, mask_kind, window, keep_first, len_ptr, ws_ptr, ws_bytes, stream_ptr) -> int:
+    """The 4-bit decode C entry point with integer pointers; returns the status code."""
+    lib = load_library()
+    c = lambda p: None if p is None else ctypes.c_void_p(int(p))  # noqa: E731
+    return lib.attn_decode_kv4(c(q_ptr), c(kc_ptr), c(ks_ptr), c(vc_ptr), c(vs_ptr), c(out_ptr), c(lse_ptr), int(N),
+                               int(Hq), int(H), int(L), int(S), int(C), int(E), int(Ev), float(scale), int(mode),
+                               c(sink_ptr), int(mask_kind), int(window), int(keep_first), c(len_ptr), c(ws_ptr),
+                               int(ws_bytes), c(stream_ptr))
+
+
+def attn_kv4_write(cache, k: torch.Tensor, v: torch.Tensor, *, start: int = 0, pos: torch.Tensor | None = None,
+                   count: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> None:
+    """Rounds new rows k (N, H, L, E), v (N, H, L, Ev) to 4 bits and stores them in the cache.
+
+    k, v: bfloat16 or float32 CUDA tensors, the last dimension contiguous, any
+    other strides that are multiples of 16 bytes (a slice of a fused projection,
+    transposed, needs no copy).  Row l of sequence n goes to cache row pos[n] + l
+    (pos (N,) int32 CUDA), or start + l without pos; with count (N,) int32 only
+    its first count[n] rows are written.  Rows outside the cache are not written.
+    """
+    N, H, C, E, Ev = _cache_shape(cache)
+    dev = cache[0].device
+    if k.dim() != 4 or v.dim() != 4 or k.shape[:2] != (N, H) or v.shape[:3] != k.shape[:3]:
+        raise ValueError("k and v must be (N, H, L, E) and (N, H, L, Ev) with the cache's N and H")
+    if k.shape[3] != E or v.shape[3] != Ev:
+        raise ValueError("k or v has another head dimension than the cache")
+    if k.dtype not in DTYPES or v.dtype != k.dtype:
+        raise ValueError("k, v must share dtype bfloat16 or float32")
+    if k.device != dev or v.device != dev:
+        raise ValueError(f"k and v must be on {dev} with the cache")
+    ks, vs = k.stride(), v.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("the last dimension of k and v must be contiguous")
+    _check_index("pos", pos, N, dev)
+    _check_index("count", count, N, dev)
+    _same_stream_device(stream, dev)
+    lib = load_library()
+    with _on(dev, stream):
+        st = lib.attn_kv4_write(k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in cache), N, H, k.shape[2], C, E, Ev,
+                                ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], _int32("start", start),
+                                None if pos is None else pos.data_ptr(), None if count is None else count.data_ptr(),
+                                DTYPES[k.dtype], torch.cuda.current_stream(dev).cuda_stream)
+    _check(st)
+
+
+def attn_kv4_read(cache, rows: int, *, start: int = 0, pos: torch.Tensor | None = None,
+                  kv_len: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16,
+                  k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+                  stream: torch.cuda.Stream | None = None):
+    """`rows` cache rows of every (batch, KV head) from row pos[n] (or start): (k, v) of shapes
+    (N, H, rows, E) and (N, H, rows, Ev) in `dtype` (bfloat16 or float32; both hold the values exactly).
+
+    Rows at or after kv_len[n] ((N,) int32 CUDA) and rows outside the cache come
+    back as 0.  k_out and v_out may be given (contiguous, of `dtype`).
+    """
+    N, H, C, E, Ev = _cache_shape(cache)
+    dev = cache[0].device
+    if dtype not in DTYPES:
+        raise ValueError("dtype must be bfloat16 or float32")
+    rows = _int32("rows", rows)
+    _check_index("pos", pos, N, dev)
+    _check_index("kv_len", kv_len, N, dev)
+    _same_stream_device(stream, dev)
+    lib = load_library()
+    with _on(dev, stream):
+        k_out = _output("k_out", k_out, (N, H, rows, E), dtype, dev)
+        v_out = _output("v_out", v_out, (N, H, rows, Ev), dtype, dev)
+        st = lib.attn_kv4_read(*(t.data_ptr() for t in cache), k_out.data_ptr(), v_out.data_ptr(), N, H, rows, C, E, Ev,
+                               _int32("start", start), None if pos is None else pos.data_ptr(),
+                               None if kv_len is None else kv_len.data_ptr(), DTYPES[dtype],
+                               torch.cuda.current_stream(dev).cuda_stream)
+    _check(st)
+    return k_out, v_out
+
+
+def _output(name, t, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+    return t
+
+
+_kv4_workspaces: dict = {}  # (device index, stream handle) -> workspace
+
+
+def kv4_workspace(device="cuda") -> torch.Tensor:
+    """A workspace for attn_decode_kv4, ready for use on the current stream (zeroed there)."""
+    return torch.zeros(load_library().attn_decode_kv4_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def _kv4_stream_workspace(device, handle):
+    """The workspace of calls on one stream.  A captured call gets one of its own, which lives in the graph's
+    memory: replays may overlap calls on the stream that the graph was captured on."""
+    if torch.cuda.is_current_stream_capturing():
+        return kv4_workspace(device)
+    key = (device.index, handle)
+    ws = _kv4_workspaces.get(key)
+    if ws is None:
+        ws = _kv4_workspaces.setdefault(key, kv4_workspace(device))
+    return ws
+
+
+def attn_decode_kv4(q: torch.Tensor, cache, *, scale: float, length: int | None = None,
+                    kv_len: torch.Tensor | None = None, mode: str = "dot", sink: torch.Tensor | None = None,
+                    mask_kind: str = "none", window: int = 0, keep_first: int = 0, out: torch.Tensor | None = None,
+                    lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    stream: torch.cuda.Stream | None = None):
+    """Decode attention straight from a 4-bit cache.  Returns (out, lse).
+
+    q (N, Hq, L, E): contiguous bfloat16 CUDA tensor with (Hq/H)*L <= 16.  length:
+    cached rows of the longest sequence (default: the capacity); kv_len (N,) int32:
+    the rows of each sequence, at most length.  Query row i of sequence n is at
+    position kv_len[n] - L + i, so the L new tokens' own rows are written first
+    (attn_kv4_write) and counted.  mode, sink, mask_kind ("none", "causal",
+    "window", "streaming"), window and keep_first as in attn_fwd.  workspace: a
+    kv4_workspace() that no overlapping call uses (default: one per stream, and one
+    of its own for a captured call).
+    """
+    _check_kinds(mode, mask_kind, keep_first)
+    N, H, C, E, Ev = _cache_shape(cache)
+    dev = cache[0].device
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or q.device != dev or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous 4-D bfloat16 tensor on {dev} with the cache")
+    Nq, Hq, L, Eq = q.shape
+    if Nq != N or Eq != E:
+        raise ValueError("q has another batch or head dimension than the cache")
+    S = C if length is None else _int32("length", length)
+    _check_index("kv_len", kv_len, N, dev)
+    if sink is not None and (sink.dtype != torch.float32 or sink.numel() != Hq or sink.device != dev
+                             or not sink.is_contiguous()):
+        raise ValueError(f"sink must be a contiguous float32 tensor of Hq values on {dev}")
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    _same_stream_device(stream, dev)
+    lib = load_library()
+    with _on(dev, stream):
+        out = _output("out", out, (N, Hq, L, Ev), torch.bfloat16, dev)
+        lse = _output("lse", lse, (N, Hq, L), torch.float32, dev)
+        handle = torch.cuda.current_stream(dev).cuda_stream
+        ws = _kv4_stream_workspace(dev, handle) if workspace is None else workspace
+        kind = "window" if mask_kind == "streaming" else mask_kind
+        kc, ks, vc, vs = cache
+        st = lib.attn_decode_kv4(q.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
+                                 out.data_ptr(), lse.data_ptr(), N, Hq, H, L, S, C, E, Ev, float(scale),
+                                 MODES[mode], None if sink is None else sink.data_ptr(), MASKS[kind],
+                                 _int32("window", window), _int32("keep_first", keep_first),
+                                 None if kv_len is None else kv_len.data_ptr(), ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), handle)
+    _check(st)
+    return out, lse
+
+
 def attn_decode_fwd_noalloc_raw(q_ptr, k_ptr, v_ptr, out_ptr, lse_ptr, N, Hq, H, L, S, E, Ev, scale, mode,
                                 sink_ptr, mask_kind, window, bias_ptr, stream_ptr) -> int:
     """The allocation-free decode entry point with integer pointers; returns the status.
@@ -384,6 +634,7 @@ def device_status(stream: torch.cuda.Stream | None = None) -> int:
 
 def release_workspace():
     load_library().attn_release_workspace()
+    _kv4_workspaces.clear()
 
 
 def version() -> int:

@@ -130,6 +130,25 @@ int validate(const void* q, const void* k, const void* v, void* out, float* lse,
   return ATTN_OK;
 }
 
+// Checks shared by the writing and reading of the 4-bit cache: `rows` new or returned rows per
+// (n, h), and the two optional per-sequence index arrays.
+int validate_kv4(const void* k, const void* v, const void* k_codes, const void* k_scales, const void* v_codes,
+                 const void* v_scales, int N, int H, int rows, int C, int E, int Ev, int dtype, const int* i0,
+                 const int* i1) {
+  if (N < 1 || H < 1 || rows < 1) return ATTN_ERR_BAD_SHAPE;  // before the pointers: empty tensors have none
+  if (!k || !v || !k_codes || !k_scales || !v_codes || !v_scales) return ATTN_ERR_NULL_POINTER;
+  if ((E != 64 && E != 128) || (Ev != 64 && Ev != 128)) return ATTN_ERR_HEAD_DIM;
+  if (C < 1 || C % 16 != 0) return ATTN_ERR_CAPACITY;
+  if (dtype != ATTN_BF16 && dtype != ATTN_FP32) return ATTN_ERR_DTYPE;
+  // the kernels number the rows of the call in 32 bits and compute offsets in 64
+  const long long nh = static_cast<long long>(N) * H, most = (1LL << 31) - 1;
+  if (nh > most || nh * rows > most || nh * C > (1LL << 40)) return ATTN_ERR_BAD_SHAPE;
+  for (const void* p : {k, v, k_codes, k_scales, v_codes, v_scales})
+    if (!aligned(p, 16)) return ATTN_ERR_ALIGNMENT;
+  if ((i0 && !aligned(i0, 4)) || (i1 && !aligned(i1, 4))) return ATTN_ERR_ALIGNMENT;
+  return ATTN_OK;
+}
+
 AttnArgs make_args(const void* q, const void* k, const void* v, void* out, float* lse, int N, int Hq, int H, int L,
                    int S, int E, int Ev, float scale, int mode, const float* sink_logits, int mask_kind, int window,
                    int keep, const float* bias, const uint32_t* mask_bits = nullptr, const int* kv_start = nullptr,
@@ -306,6 +325,68 @@ int attn_decode_indexed(const void* q, const void* k, const void* v, void* out, 
   return launch_decode_gather_bf16(a, key_idx, n_sel, ws, need, sms, stream);
 }
 
+int attn_kv4_write(const void* k, const void* v, void* k_codes, void* k_scales, void* v_codes, void* v_scales, int N,
+                   int H, int L, int C, int E, int Ev, size_t k_stride_n, size_t k_stride_h, size_t k_stride_l,
+                   size_t v_stride_n, size_t v_stride_h, size_t v_stride_l, int start, const int* pos,
+                   const int* count, int dtype, void* stream_ptr) {
+  using namespace attn;
+  int st = validate_kv4(k, v, k_codes, k_scales, v_codes, v_scales, N, H, L, C, E, Ev, dtype, pos, count);
+  if (st != ATTN_OK) return st;
+  // a dimension of one entry is never stepped through
+  if (N == 1) k_stride_n = v_stride_n = 0;
+  if (H == 1) k_stride_h = v_stride_h = 0;
+  if (L == 1) k_stride_l = v_stride_l = 0;
+  const size_t per16 = dtype == ATTN_BF16 ? 8 : 4;
+  if ((k_stride_n | k_stride_h | k_stride_l | v_stride_n | v_stride_h | v_stride_l) % per16) return ATTN_ERR_ALIGNMENT;
+  int dev = 0, sms = 0, major = 0;
+  if (device_info(&dev, &sms, &major) != ATTN_OK) return ATTN_ERR_CUDA;
+  if (major != 10) return ATTN_ERR_DEVICE;
+  const Kv4WriteArgs a{k,          v,          k_codes,    k_scales,   v_codes,    v_scales,   N,     H,   L,    C, E, Ev,
+                       k_stride_n, k_stride_h, k_stride_l, v_stride_n, v_stride_h, v_stride_l, start, pos, count};
+  return launch_kv4_write(a, dtype == ATTN_BF16, static_cast<cudaStream_t>(stream_ptr));
+}
+
+int attn_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales, void* k, void* v,
+                  int N, int H, int rows, int C, int E, int Ev, int start, const int* pos, const int* kv_len,
+                  int dtype, void* stream_ptr) {
+  using namespace attn;
+  int st = validate_kv4(k, v, k_codes, k_scales, v_codes, v_scales, N, H, rows, C, E, Ev, dtype, pos, kv_len);
+  if (st != ATTN_OK) return st;
+  int dev = 0, sms = 0, major = 0;
+  if (device_info(&dev, &sms, &major) != ATTN_OK) return ATTN_ERR_CUDA;
+  if (major != 10) return ATTN_ERR_DEVICE;
+  const Kv4ReadArgs a{k_codes, k_scales, v_codes, v_scales, k, v, N, H, rows, C, E, Ev, start, pos, kv_len};
+  return launch_kv4_read(a, dtype == ATTN_BF16, static_cast<cudaStream_t>(stream_ptr));
+}
+
+int attn_decode_kv4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                    void* out, float* lse, int N, int Hq, int H, int L, int S, int C, int E, int Ev, float scale,
+                    int mode, const float* sink_logits, int mask_kind, int window, int keep_first, const int* kv_len,
+                    void* workspace, size_t workspace_bytes, void* stream_ptr) {
+  using namespace attn;
+  if (!k_scales || !v_scales || !workspace) return ATTN_ERR_NULL_POINTER;
+  if (mask_kind < ATTN_MASK_NONE || mask_kind > ATTN_MASK_SLIDING_WINDOW) return ATTN_ERR_MASK;
+  if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window < 1) return ATTN_ERR_WINDOW;
+  if (keep_first < 0 || (keep_first > 0 && mask_kind != ATTN_MASK_SLIDING_WINDOW)) return ATTN_ERR_KEEP;
+  int st = validate(q, k_codes, v_codes, out, lse, N, Hq, H, L, S, E, Ev, scale, mode, sink_logits, nullptr, ATTN_BF16);
+  if (st != ATTN_OK) return st;
+  if (C < 1 || C % 16 != 0 || S > C) return ATTN_ERR_CAPACITY;
+  if (static_cast<long long>(N) * H * C > (1LL << 40)) return ATTN_ERR_BAD_SHAPE;
+  if (!aligned(k_scales, 16) || !aligned(v_scales, 16) || !aligned(workspace, 16) || (kv_len && !aligned(kv_len, 4)))
+    return ATTN_ERR_ALIGNMENT;
+  if (static_cast<long long>(Hq / H) * L > 16) return ATTN_ERR_NOT_DECODE;
+  if (workspace_bytes < kv4_decode_workspace_bytes()) return ATTN_ERR_WORKSPACE_SIZE;
+  int dev = 0, sms = 0, major = 0;
+  if (device_info(&dev, &sms, &major) != ATTN_OK) return ATTN_ERR_CUDA;
+  if (major != 10) return ATTN_ERR_DEVICE;
+  const Kv4DecodeArgs a{q, k_codes, k_scales, v_codes, v_scales, out, lse, N, Hq, H, L, S, C, E, Ev, scale,
+                        mode == ATTN_RBF, sink_logits, keep_first > 0 ? MASK_STREAM : mask_kind, window, keep_first,
+                        kv_len};
+  return launch_kv4_decode(a, workspace, sms, static_cast<cudaStream_t>(stream_ptr));
+}
+
+size_t attn_decode_kv4_workspace_bytes(void) { return attn::kv4_decode_workspace_bytes(); }
+
 const char* attn_status_string(int status) {
   switch (status) {
     case ATTN_OK: return "ok";
@@ -327,6 +408,8 @@ const char* attn_status_string(int status) {
     case ATTN_ERR_DEVICE: return "device is not compute capability 10.x (B200)";
     case ATTN_ERR_SCRATCH_LIMIT: return "the call needs more scratch than the fixed no-allocation area holds";
     case ATTN_ERR_NOT_DECODE: return "not a decode-shaped bf16 call ((Hq/H)*L must be <= 16)";
+    case ATTN_ERR_CAPACITY: return "the 4-bit cache's capacity must be a positive multiple of 16 and hold the rows asked for";
+    case ATTN_ERR_WORKSPACE_SIZE: return "the given workspace is too small";
     default: return "unknown status";
   }
 }
@@ -353,8 +436,9 @@ int attn_device_status(void* stream_ptr) {
   const unsigned int a = take_status_prefill(s);
   const unsigned int b = take_status_decode(s);
   const unsigned int c = take_status_bwd(s);
-  if (a == 0xFFFFFFFFu || b == 0xFFFFFFFFu || c == 0xFFFFFFFFu) return ATTN_ERR_CUDA;
-  return (a | b | c) ? ATTN_ERR_DEVICE_TIMEOUT : ATTN_OK;
+  const unsigned int d = take_status_kv4(s);
+  if (a == 0xFFFFFFFFu || b == 0xFFFFFFFFu || c == 0xFFFFFFFFu || d == 0xFFFFFFFFu) return ATTN_ERR_CUDA;
+  return (a | b | c | d) ? ATTN_ERR_DEVICE_TIMEOUT : ATTN_OK;
 }
 
 int attn_version(void) { return 10000; }

@@ -93,6 +93,54 @@ size_t bwd_workspace_bytes(const BwdArgs& a);
 int launch_bwd_bf16(const BwdArgs& a, void* workspace, cudaStream_t stream);
 unsigned int take_status_bwd(cudaStream_t s);
 
+// The 4-bit cache (kv4.cuh): codes [N*H][C][E/2] bytes and scales [N*H][C][E/16] bytes for K,
+// the same with Ev for V.
+struct Kv4WriteArgs {
+  const void* k;  // value (n, h, l, e) at n*k_sn + h*k_sh + l*k_sl + e
+  const void* v;
+  void* k_codes;
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  int N, H, L, C, E, Ev;
+  size_t k_sn, k_sh, k_sl, v_sn, v_sh, v_sl;
+  int start;
+  const int* pos;    // [N] cache row of l = 0, or nullptr (start)
+  const int* count;  // [N] rows written per sequence, or nullptr (L)
+};
+struct Kv4ReadArgs {
+  const void* k_codes;
+  const void* k_scales;
+  const void* v_codes;
+  const void* v_scales;
+  void* k;  // [N, H, rows, E]
+  void* v;  // [N, H, rows, Ev]
+  int N, H, rows, C, E, Ev;
+  int start;
+  const int* pos;     // [N] first cache row read, or nullptr (start)
+  const int* kv_len;  // [N] valid rows (others read as 0), or nullptr (C)
+};
+struct Kv4DecodeArgs {
+  const void* q;
+  const void* k_codes;
+  const void* k_scales;
+  const void* v_codes;
+  const void* v_scales;
+  void* out;
+  float* lse;
+  int N, Hq, H, L, S, C, E, Ev;
+  float scale;
+  bool rbf;
+  const float* sink;  // [Hq] or nullptr
+  int mask_kind, window, keep;
+  const int* kv_len;  // [N] or nullptr (S)
+};
+int launch_kv4_write(const Kv4WriteArgs& a, bool bf16, cudaStream_t stream);
+int launch_kv4_read(const Kv4ReadArgs& a, bool bf16, cudaStream_t stream);
+size_t kv4_decode_workspace_bytes();
+int launch_kv4_decode(const Kv4DecodeArgs& a, void* workspace, int num_sms, cudaStream_t stream);
+unsigned int take_status_kv4(cudaStream_t s);
+
 unsigned int take_status_prefill(cudaStream_t s);
 // A kernel whose one bounded wait runs out after limit_cycles (failure-path check).
 int launch_wait_timeout_test(int limit_cycles, cudaStream_t stream);

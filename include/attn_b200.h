@@ -67,7 +67,9 @@ typedef enum {
   ATTN_ERR_DEVICE = -15,        /* the current device is not sm_100 */
   ATTN_ERR_SCRATCH_LIMIT = -16, /* attn_decode_fwd_noalloc: the call needs more scratch than the fixed area holds */
   ATTN_ERR_NOT_DECODE = -17,    /* attn_decode_fwd_noalloc / attn_decode_indexed: not a decode-shaped bf16 call ((Hq/H)*L <= 16) */
-  ATTN_ERR_KEEP = -18           /* keep_first < 0 (attn_fwd_streaming, attn_bwd), or kept keys without a window (attn_bwd) */
+  ATTN_ERR_KEEP = -18,          /* keep_first < 0 (attn_fwd_streaming, attn_bwd, attn_decode_kv4), or kept keys without a window (the latter two) */
+  ATTN_ERR_CAPACITY = -19,      /* a 4-bit cache's capacity C is not a positive multiple of 16, or is less than the rows asked for */
+  ATTN_ERR_WORKSPACE_SIZE = -20 /* attn_decode_kv4: the given workspace is smaller than attn_decode_kv4_workspace_bytes() */
 } attn_status;
 
 /*
@@ -232,6 +234,97 @@ int attn_decode_indexed(const void* q, const void* k, const void* v, void* out, 
                         int N, int Hq, int H, int L, int S, int E, int Ev, float scale,
                         const float* sink_logits, int mask_kind, int window, const float* bias,
                         void* stream);
+
+/*
+ * The 4-bit key/value cache: attn_kv4_write appends K and V rows to it,
+ * attn_kv4_read brings rows back, attn_decode_kv4 attends to it (page "SDPA란
+ * 무엇인가" section 4: a decode step appends the new key and value to the cache and
+ * attends to all of it; the pages keep the cache in the tensors' own type, the
+ * 4-bit form is this library's).
+ *
+ * Layout, all device memory owned by the caller, contiguous, C rows of capacity
+ * for each (batch, KV head):
+ *   k_codes  [N, H, C, E/2]   bytes    k_scales [N, H, C, E/16]   bytes
+ *   v_codes  [N, H, C, Ev/2]  bytes    v_scales [N, H, C, Ev/16]  bytes
+ * 4.5 bits per value.  C is a multiple of 16; all four are 16-byte aligned.  A row
+ * is cut into blocks of 16 values.  A block x stands for c_i * s:
+ *   s    one byte, 5 exponent bits (bias 15) and 3 mantissa bits: the byte shifted
+ *        left by 7 is its fp16 pattern.  It is the scale nearest to max|x| / 6
+ *        (ties to even), at most 10240 (byte 226).
+ *   c_i  4 bits, a sign and one of 0, .5, 1, 1.5, 2, 3, 4, 6 (code 0 to 7): the
+ *        nearest to x_i / s (ties to the even code), at most 6; 0 where s = 0.
+ *        Element 2i of a row is the low half of byte i.
+ * Values beyond +-61440, infinities among them, are held as +-61440; a block with a
+ * NaN has the scale byte 255 and reads back as 16 NaN.  Every c_i * s is exact in
+ * fp16, bf16 and fp32.
+ *
+ * attn_kv4_write -- rounds new rows and stores them.
+ *   k, v    new rows in `dtype` (ATTN_BF16 or ATTN_FP32); value e of row l of
+ *           (n, h) is at n*k_stride_n + h*k_stride_h + l*k_stride_l + e elements
+ *           (v likewise), so a slice of a fused projection needs no copy.  The
+ *           strides are multiples of 16 bytes (0 repeats a row); that of a
+ *           dimension of size 1 is not used.
+ *   L       new rows per sequence (>= 1)
+ *   pos     [N] int32, device, or NULL: the cache row of row l = 0 of sequence n is
+ *           pos[n], or `start` for all with NULL
+ *   count   [N] int32, device, or NULL: only the first count[n] of the L rows are
+ *           written (ragged prompts; <= 0 writes none); NULL writes all
+ * Row l goes to cache row pos[n] + l of sequence n; a row outside [0, C) is not
+ * written.  No other byte of the cache changes.
+ *
+ * attn_kv4_read -- brings back `rows` consecutive cache rows of every (n, h).
+ *   k [N, H, rows, E], v [N, H, rows, Ev]  contiguous outputs in `dtype`
+ *   pos, start  the first cache row, as above
+ *   kv_len  [N] int32, device, or NULL (C): rows at or after kv_len[n], and rows
+ *           outside [0, C), come back as 0 whatever the cache holds there, so the
+ *           outputs can go to attn_fwd_padded with kv_end
+ *
+ * Both validate first and launch nothing on error, need no workspace, and return
+ * without a host synchronisation.  Errors: ATTN_ERR_NULL_POINTER,
+ * ATTN_ERR_BAD_SHAPE (a size < 1, or N*H*L (N*H*rows) or N*H >= 2^31),
+ * ATTN_ERR_HEAD_DIM (E or Ev not in {64, 128}), ATTN_ERR_CAPACITY (C not a positive
+ * multiple of 16), ATTN_ERR_DTYPE, ATTN_ERR_ALIGNMENT (tensors, cache and strides 16
+ * bytes, pos, count and kv_len 4), and attn_fwd's device errors.
+ */
+int attn_kv4_write(const void* k, const void* v, void* k_codes, void* k_scales, void* v_codes, void* v_scales,
+                   int N, int H, int L, int C, int E, int Ev, size_t k_stride_n, size_t k_stride_h,
+                   size_t k_stride_l, size_t v_stride_n, size_t v_stride_h, size_t v_stride_l, int start,
+                   const int* pos, const int* count, int dtype, void* stream);
+int attn_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales, void* k,
+                  void* v, int N, int H, int rows, int C, int E, int Ev, int start, const int* pos,
+                  const int* kv_len, int dtype, void* stream);
+
+/*
+ * attn_decode_kv4 -- decode attention straight from the 4-bit cache, without a
+ * bf16 copy of it: attn_fwd's formula on the values the cache stands for.
+ *   q, out  [N, Hq, L, E] and [N, Hq, L, Ev] bf16, lse [N, Hq, L] float or NULL
+ *   S       the longest sequence's cached rows (1 <= S <= C)
+ *   kv_len  [N] int32, device, or NULL (S): the cached rows of each sequence,
+ *           clamped to [0, S].  Query row i of sequence n sits at position
+ *           kv_len[n] - L + i and keys j >= kv_len[n] are not visible: with L new
+ *           tokens, call attn_kv4_write first and count them in kv_len.
+ *   scale, mode, sink_logits  as in attn_fwd
+ *   mask_kind, window, keep_first  as in attn_bwd: kept initial keys go with
+ *           ATTN_MASK_SLIDING_WINDOW (the streaming mask)
+ *   workspace  device memory of attn_decode_kv4_workspace_bytes() bytes, 16-byte
+ *           aligned, filled with zeros before its first use; every call leaves it
+ *           ready for the next.  Calls that share a workspace must be ordered;
+ *           calls with workspaces of their own may overlap, captured or not.
+ * A key that the masks hide from a row takes no part in it, whatever the cache
+ * holds (blocks with a NaN among them).  A row that sees no key gets out = 0 and
+ * lse = -inf (lse = s with a sink).  The call must be decode-shaped,
+ * (Hq/H)*L <= 16, else ATTN_ERR_NOT_DECODE: for longer query blocks read the rows
+ * back (attn_kv4_read) and use attn_fwd.  Other errors: attn_fwd's codes,
+ * ATTN_ERR_KEEP, ATTN_ERR_CAPACITY, ATTN_ERR_WORKSPACE_SIZE.  Nothing is allocated
+ * and the host is not synchronised.
+ */
+int attn_decode_kv4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
+                    const void* v_scales, void* out, float* lse, int N, int Hq, int H, int L, int S, int C, int E,
+                    int Ev, float scale, int mode, const float* sink_logits, int mask_kind, int window,
+                    int keep_first, const int* kv_len, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that attn_decode_kv4 needs, the same for every call. */
+size_t attn_decode_kv4_workspace_bytes(void);
 
 /* Human-readable text for a status code (static storage, never NULL). */
 const char* attn_status_string(int status);
