@@ -45,7 +45,8 @@ namespace {
 constexpr int KC = 64;                    // keys per chunk
 constexpr int NWARP = 8;                  // consumer warps
 constexpr int NCT = NWARP * 32;           // consumer threads
-constexpr int THREADS = NCT + 32;         // and the producer warp
+constexpr int NPROD = 4;                  // producer warps
+constexpr int THREADS = NCT + NPROD * 32;
 constexpr int MAX_CTAS = 160;             // grid limit, which sizes the workspace
 constexpr int MIN_CHUNKS = 4;             // a CTA's share, at least
 constexpr float RESCALE = 8.f;            // the running maximum follows the true one within 2^8
@@ -301,12 +302,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_decode_kernel(const Params p, 
   }
   __syncthreads();
 
-  if (warp == NWARP) {
-    // ---------------- producer ----------------
+  if (warp >= NWARP) {
+    // ---------------- producers: one thread each, every NPROD-th chunk ----------------
     if (lane == 0) {
       Walk w = w0;
-      int issued = 0;
-      for (long long c = c_begin; c < c_end; ++c) {
+      int issued = 0;  // of this producer's chunks
+      for (long long c = c_begin + (warp - NWARP); c < c_end; c += NPROD) {
         while (c >= w.u0 + w.s.nc) w.next(p);
         const int idx = static_cast<int>(c - c_begin);
         const int s = idx % C::NSTAGE;
@@ -324,11 +325,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_decode_kernel(const Params p, 
         bulk_load(dst + C::OFF_KS, p.k_scales + row * (E / 16), rows * (E / 16), full_bar(s));
         bulk_load(dst + C::OFF_V, p.v_codes + row * (EV / 2), rows * (EV / 2), full_bar(s));
         bulk_load(dst + C::OFF_VS, p.v_scales + row * (EV / 16), rows * (EV / 16), full_bar(s));
-        issued = idx + 1;
+        ++issued;
       }
       // drain: the last copies (one per stage) have landed before exit
-      for (int idx = issued > C::NSTAGE ? issued - C::NSTAGE : 0; idx < issued; ++idx)
+      for (int y = max(0, issued - C::NSTAGE / NPROD); y < issued; ++y) {
+        const int idx = y * NPROD + warp - NWARP;
         mbar_wait(full_bar(idx % C::NSTAGE), (idx / C::NSTAGE) & 1);
+      }
     }
     return;
   }
