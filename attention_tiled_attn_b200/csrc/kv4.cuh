@@ -48,7 +48,7 @@ __device__ __forceinline__ uint32_t kv4_pack8(const float* x) {
 }
 
 // the fp16 pair (s, s) of a scale byte
-__device__ __forceinline__ uint32_t kv4_scale2(uint32_t byte) { return (byte * 0x00010001u) << 7; }
+__device__ __forceinline__ uint32_t kv4_scale2(uint32_t byte) { return byte * 0x00800080u; }  // byte << 7 in both halves
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;

@@ -213,6 +213,29 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// mbar_wait of warps that mostly wait: the hardware suspends the thread for up to 20 us between tests, so that it
+// takes no issue slots from the consumers
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+  long long t0 = 0;
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    if (done) return true;
+    const long long t = clock64();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > WAIT_LIMIT_CYCLES) {
+      record_timeout();
+      return false;
+    }
+  }
+}
+
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -233,24 +256,24 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// the low halves of a's bytes and the high halves of b's
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, 0x0F0F0F0F, 0xE4;" : "=r"(d) : "r"(a), "r"(b));  // (a & m) | (b & ~m)
+  return d;
+}
+
 template <int BYTES>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[BYTES / 4]) {
-  if constexpr (BYTES == 16)
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
-  else if constexpr (BYTES == 8)
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-  else
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr));
-  return r;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint32_t r;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(addr));
-  return r;
+__device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[BYTES / 4]) {
+  if constexpr (BYTES == 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (BYTES == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(src);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(src);
+  }
 }
 
 __device__ __forceinline__ void merge_bar() { asm volatile("bar.sync 1, %0;" ::"n"(NMERGE * 32) : "memory"); }
@@ -413,7 +436,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     const int mt = tid - (NCW + NPROD) * 32;
     bool ok = true;
     for (; more; more = w.next(p)) {
-      ok = mbar_wait(mfull_bar, w.k & 1);
+      ok = mbar_sleep(mfull_bar, w.k & 1);
       // both warps decide together
       uint32_t both;
       asm volatile(
@@ -510,7 +533,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
       bool ok = true;
       for (; more && ok; more = w.next(p)) {
         if (q_next == w.k) {
-          ok = mbar_wait(qempty_bar(w.k), ((w.k / NQ) & 1) ^ 1) && !*abort_flag;
+          ok = mbar_sleep(qempty_bar(w.k), ((w.k / NQ) & 1) ^ 1) && !*abort_flag;
           if (!ok) break;
           const uint32_t bytes = p.R * E * 2;
           mbar_arrive_expect_tx(qfull_bar(w.k), bytes);
@@ -520,7 +543,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
         const size_t unit_row = w.unit(p) * p.C;
         for (; idx < w.i0 + (w.hi - w.lo); idx += NPROD) {
           const unsigned s = idx % C::NSTAGE;
-          ok = mbar_wait(empty_bar(s), ((idx / C::NSTAGE) & 1) ^ 1) && !*abort_flag;
+          ok = mbar_sleep(empty_bar(s), ((idx / C::NSTAGE) & 1) ^ 1) && !*abort_flag;
           if (!ok) break;
           const int key0 = w.key0(w.lo + (idx - w.i0));
           const int rows = min(KC, p.C - key0);  // a multiple of 16
@@ -560,25 +583,32 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     float o[NT][MD][4];
     float cq[NT][2], m_run[NT][2], l_run[NT][2];
     bool ok = true;
+    unsigned idx = grp, s = grp, phase = 0;  // the group's next chunk, its stage (idx % NSTAGE) and the stage's parity
+    const uint8_t* kp = smem + (j0 + kap_k) * (E / 2) + c4 * KB;  // this lane's bytes in stage 0
+    const uint8_t* ksp = smem + C::OFF_KS + (j0 + kap_k) * (E / 16) + c4 * (E / 64);
+    const uint8_t* vp0 = smem + C::OFF_V + (j0 + kap_v) * (EV / 2) + ra * VB;
+    const uint8_t* vp1 = smem + C::OFF_V + (j0 + (kap_v ^ 1)) * (EV / 2) + ra * VB;
+    const int vg = EV == 128 ? ra : ra >> 1;  // the block of 16 of this lane's value dimensions
+    const uint8_t* vsp0 = smem + C::OFF_VS + (j0 + kap_v) * (EV / 16) + vg;
+    const uint8_t* vsp1 = smem + C::OFF_VS + (j0 + (kap_v ^ 1)) * (EV / 16) + vg;
 
     for (; more && ok; more = w.next(p)) {
-      ok = __all_sync(0xffffffffu, mbar_wait(qfull_bar(w.k), (w.k / NQ) & 1));
+      ok = __all_sync(0xffffffffu, mbar_sleep(qfull_bar(w.k), (w.k / NQ) & 1));
       if (!ok) break;
       const unsigned i1 = w.i0 + (w.hi - w.lo);
-      unsigned idx = w.i0 + (grp + NG - w.i0 % NG) % NG;
       const bool mine = idx < i1;
       if (mine) {
         // Q^T's fragments: lane (row ra, column c4) takes its E / 4 dimensions, shifted to [2^14, 2^15)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const int r = ra + 8 * t;
-          const uint32_t src = sb + C::OFF_Q + (w.k % NQ) * C::Q_SLOT + (r * E + c4 * (E / 4)) * 2;
+          const uint8_t* src = smem + C::OFF_Q + (w.k % NQ) * C::Q_SLOT + (r * E + c4 * (E / 4)) * 2;
           uint32_t x[E / 8];
           float most = 0.f;
 #pragma unroll
           for (int y = 0; y < E / 32; ++y) {
             uint32_t v[4];
-            lds_words<16>(src + 16 * y, v);
+            load_words<16>(src + 16 * y, v);
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               x[4 * y + z] = r < p.R ? v[z] : 0u;
@@ -610,37 +640,31 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
       const int off = w.s.len - p.L;
       const int lo_first = windowed ? off - p.window + 1 : 0, lo_last = windowed ? off + p.L - p.window : 0;
       const int hi_first = causal ? off + 1 : w.s.len, hi_last = w.s.len;
+      // every row sees all of this warp's keys of a chunk if the first one is one of n_full from lo_last on
+      const unsigned n_full = static_cast<unsigned>(max(0, hi_first - 16 * MT - lo_last + 1));
 
-      for (; idx < i1; idx += NG) {
-        const unsigned s = idx % C::NSTAGE;
-        ok = __all_sync(0xffffffffu, mbar_wait(full_bar(s), (idx / C::NSTAGE) & 1));
+      while (idx < i1) {
+        ok = __all_sync(0xffffffffu, mbar_sleep(full_bar(s), phase));
         if (!ok) break;
-        const uint32_t stage = sb + s * C::STAGE;
+        const unsigned at = s * C::STAGE;
         const int key0 = w.key0(w.lo + (idx - w.i0)) + j0;
-        const bool masked = key0 + 16 * MT > hi_first || (key0 < lo_last && key0 + 16 * MT > p.keep);
+        const bool full = static_cast<unsigned>(key0 - lo_last) < n_full;
         // keys that no row sees need no work
-        if (key0 < hi_last && (key0 + 16 * MT > lo_first || key0 < p.keep)) {
+        if (full || (key0 < hi_last && (key0 + 16 * MT > lo_first || key0 < p.keep))) {
           float sc[MT][NT][4];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) sc[mt][t][0] = sc[mt][t][1] = sc[mt][t][2] = sc[mt][t][3] = 0.f;
             float gram[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            const int j = j0 + 16 * mt + kap_k;  // this lane's keys: j and j + 8
-            uint32_t k0[KB / 4], k1[KB / 4];
-            lds_words<KB>(stage + j * (E / 2) + c4 * KB, k0);
-            lds_words<KB>(stage + (j + 8) * (E / 2) + c4 * KB, k1);
+            uint32_t k0[KB / 4], k1[KB / 4];  // this lane's keys: 16 mt + kap_k and 8 more
+            load_words<KB>(kp + at + 16 * mt * (E / 2), k0);
+            load_words<KB>(kp + at + (16 * mt + 8) * (E / 2), k1);
             uint32_t s0[E / 64], s1[E / 64];  // (s, s) of the lane's blocks of 16
-            if constexpr (E == 128) {
-              const uint32_t b0 = lds_u16(stage + C::OFF_KS + j * 8 + c4 * 2);
-              const uint32_t b1 = lds_u16(stage + C::OFF_KS + (j + 8) * 8 + c4 * 2);
-              s0[0] = __byte_perm(b0, 0, 0x4040) << 7;
-              s0[1] = __byte_perm(b0, 0, 0x4141) << 7;
-              s1[0] = __byte_perm(b1, 0, 0x4040) << 7;
-              s1[1] = __byte_perm(b1, 0, 0x4141) << 7;
-            } else {
-              s0[0] = kv4_scale2(lds_u8(stage + C::OFF_KS + j * 4 + c4));
-              s1[0] = kv4_scale2(lds_u8(stage + C::OFF_KS + (j + 8) * 4 + c4));
+#pragma unroll
+            for (int x = 0; x < E / 64; ++x) {
+              s0[x] = kv4_scale2(ksp[at + 16 * mt * (E / 16) + x]);
+              s1[x] = kv4_scale2(ksp[at + (16 * mt + 8) * (E / 16) + x]);
             }
 #pragma unroll
             for (int x = 0; x < KB / 4; ++x) {
@@ -676,43 +700,100 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
                 sc[mt][t][3] = fmaf(sc[mt][t][3], 2.f * cq[t][1], -n1);
               }
             }
-            if (masked) {
-              const int key = key0 + 16 * mt + kap_k;
+          }
+          // scales of V: keys kap_v, kap_v ^ 1 (fragment rows 2 c4, 2 c4 + 1) and both + 8, as pairs
+          uint32_t vs[MT][2];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const int x = (16 * mt + 8 * z) * (EV / 16);
+              vs[mt][z] = vsp0[at + x] | (static_cast<uint32_t>(vsp1[at + x]) << 16);
+            }
+          if (!full) {
+            auto seen_by = [&](int key, int row_at) {
+              return key < hi_last && !(causal && key > row_at) && !(windowed && key <= row_at - p.window && key >= p.keep);
+            };
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
               for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int x = key + (e >> 1) * 8, row_at = off + qi[t][e & 1];
-                  if ((causal && x > row_at) || x >= hi_last || (windowed && x <= row_at - p.window && x >= p.keep))
-                    sc[mt][t][e] = -INFINITY;
+                for (int e = 0; e < 4; ++e)
+                  if (!seen_by(key0 + 16 * mt + kap_k + (e >> 1) * 8, off + qi[t][e & 1])) sc[mt][t][e] = -INFINITY;
+              // V of a key that no row sees has weight 0 and a scale that may be anything: 0 stands in for it.
+              // A NaN block that only some rows see is added to those rows by itself.
+              bool odd = false;
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                uint32_t both = 0;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const int key = key0 + 16 * mt + (kap_v ^ x) + 8 * z;
+                  const uint32_t b = (vs[mt][z] >> (16 * x)) & 0xFFu;
+                  const bool seen = key < hi_last && (key >= lo_first || key < p.keep);
+                  odd = odd || (seen && b > KV4_MAX_SCALE);
+                  if (seen && b <= KV4_MAX_SCALE) both |= b << (16 * x);
                 }
+                vs[mt][z] = both;
+              }
+              if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+                for (int y = 0; y < 16; ++y) {
+                  const int j = 16 * mt + y;
+                  if (smem[at + C::OFF_VS + (j0 + j) * (EV / 16) + vg] <= KV4_MAX_SCALE) continue;
+#pragma unroll
+                  for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                      if (seen_by(key0 + j, off + qi[t][e])) {
+#pragma unroll
+                        for (int d = 0; d < MD; ++d) o[t][d][e] = o[t][d][e + 2] = __int_as_float(0x7fffffff);
+                      }
+                }
+              }
             }
           }
-          // online softmax over the tiles' keys (the running maximum moves only by more than 2^RESCALE)
-          uint32_t pt[MT][NT][2];
+          // online softmax over the tiles' keys.  The running maximum moves only when some logit exceeds it by more
+          // than RESCALE, which one vote of the warp decides; only then the lanes' maxima are reduced.
+          float mx[NT][2];
+          bool over = false;
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            float bias[2], cc[2];
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(sc[0][t][e], sc[0][t][e + 2]);
+              mx[t][e] = fmaxf(sc[0][t][e], sc[0][t][e + 2]);
 #pragma unroll
-              for (int mt = 1; mt < MT; ++mt) mx = fmax3(mx, sc[mt][t][e], sc[mt][t][e + 2]);
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              cc[e] = RBF ? 1.f : cq[t][e];
-              const float m_new = fmaxf(m_run[t][e], mx * cc[e]);
-              if (m_new > m_run[t][e] + RESCALE) {
-                const float f = ex2(m_run[t][e] - m_new);
+              for (int mt = 1; mt < MT; ++mt) mx[t][e] = fmax3(mx[t][e], sc[mt][t][e], sc[mt][t][e + 2]);
+              if constexpr (!RBF) mx[t][e] *= cq[t][e];
+              over = over || mx[t][e] > m_run[t][e] + RESCALE;
+            }
+          if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float m = fmaxf(m_run[t][e], mx[t][e]);
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                const float f = m > m_run[t][e] ? ex2(m_run[t][e] - m) : 1.f;
                 l_run[t][e] *= f;
 #pragma unroll
                 for (int d = 0; d < MD; ++d) {
                   o[t][d][e] *= f;
                   o[t][d][e + 2] *= f;
                 }
-                m_run[t][e] = m_new;
+                m_run[t][e] = m;
               }
+          }
+          uint32_t pt[MT][NT][2];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float bias[2], cc[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              cc[e] = RBF ? 1.f : cq[t][e];
               bias[e] = P_SHIFT - (m_run[t][e] == -INFINITY ? 0.f : m_run[t][e]);
             }
 #pragma unroll
@@ -728,51 +809,21 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
           // O^T += V^T P^T
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            uint32_t v[4][VB / 4], b[4];
+            uint32_t v[4][VB / 4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {  // keys of fragment rows 2 c4, 2 c4 + 1, and both + 8
-              const int j = j0 + 16 * mt + (kap_v ^ (x & 1)) + (x >> 1) * 8;
-              lds_words<VB>(stage + C::OFF_V + j * (EV / 2) + ra * VB, v[x]);
-              b[x] = lds_u8(stage + C::OFF_VS + j * (EV / 16) + (EV == 128 ? ra : ra >> 1));
+            for (int z = 0; z < 2; ++z) {
+              load_words<VB>(vp0 + at + (16 * mt + 8 * z) * (EV / 2), v[2 * z]);
+              load_words<VB>(vp1 + at + (16 * mt + 8 * z) * (EV / 2), v[2 * z + 1]);
             }
-            if (masked) {
-              // a key that no row sees has weight 0 and a scale that may be anything: 0 stands in for it.
-              // A NaN block that only some rows see is added to those rows by itself.
-              bool odd = false;
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const int key = key0 + 16 * mt + (kap_v ^ (x & 1)) + (x >> 1) * 8;
-                const bool seen = key < hi_last && (key >= lo_first || key < p.keep);
-                odd = odd || (seen && b[x] > KV4_MAX_SCALE);
-                if (!seen || b[x] > KV4_MAX_SCALE) b[x] = 0;
-              }
-              if (__any_sync(0xffffffffu, odd)) {
-#pragma unroll 1
-                for (int y = 0; y < 16; ++y) {
-                  const int j = j0 + 16 * mt + y, key = key0 + 16 * mt + y;
-                  if (lds_u8(stage + C::OFF_VS + j * (EV / 16) + (EV == 128 ? ra : ra >> 1)) <= KV4_MAX_SCALE) continue;
-#pragma unroll
-                  for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                      const int row_at = off + qi[t][e];
-                      if ((causal && key > row_at) || key >= hi_last || (windowed && key <= row_at - p.window && key >= p.keep))
-                        continue;
-#pragma unroll
-                      for (int d = 0; d < MD; ++d) o[t][d][e] = o[t][d][e + 2] = __int_as_float(0x7fffffff);
-                    }
-                }
-              }
-            }
-            const uint32_t sa = (b[0] + (b[1] << 16)) << 7, sz = (b[2] + (b[3] << 16)) << 7;
+            const uint32_t sa = vs[mt][0] << 7, sz = vs[mt][1] << 7;
 #pragma unroll
             for (int x = 0; x < VB / 4; ++x) {
               // bytes with one dimension's elements of two keys: even dimensions, odd dimensions
               uint32_t ea[4], oa[4], ez[4], oz[4];
-              kv4_unpack8((v[0][x] & 0x0F0F0F0Fu) | ((v[1][x] << 4) & 0xF0F0F0F0u), ea);
-              kv4_unpack8(((v[0][x] >> 4) & 0x0F0F0F0Fu) | (v[1][x] & 0xF0F0F0F0u), oa);
-              kv4_unpack8((v[2][x] & 0x0F0F0F0Fu) | ((v[3][x] << 4) & 0xF0F0F0F0u), ez);
-              kv4_unpack8(((v[2][x] >> 4) & 0x0F0F0F0Fu) | (v[3][x] & 0xF0F0F0F0u), oz);
+              kv4_unpack8(low_halves(v[0][x], v[1][x] << 4), ea);
+              kv4_unpack8(low_halves(v[0][x] >> 4, v[1][x]), oa);
+              kv4_unpack8(low_halves(v[2][x], v[3][x] << 4), ez);
+              kv4_unpack8(low_halves(v[2][x] >> 4, v[3][x]), oz);
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 const uint32_t a[4] = {hmul2(ea[y], sa), hmul2(oa[y], sa), hmul2(ez[y], sz), hmul2(oz[y], sz)};
@@ -784,11 +835,17 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty_bar(s));
+        idx += NG;
+        s += NG;
+        if (s >= C::NSTAGE) {
+          s -= C::NSTAGE;
+          phase ^= 1;
+        }
       }
       if (!ok) break;
       // hand the state to the merging warps, once they have read the last one
       if (w.k > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(mempty_bar, (w.k - 1) & 1));
+        ok = __all_sync(0xffffffffu, mbar_sleep(mempty_bar, (w.k - 1) & 1));
         if (!ok) break;
       }
       if (mine) {
