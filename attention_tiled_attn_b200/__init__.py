@@ -400,19 +400,27 @@ def _int32(name: str, x) -> int:
     return x
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(device) -> int:
+    """The cudaStream_t of the device's current stream."""
+    return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device.index)
+
+
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or torch.cuda.current_device() != device.index
+
+
+@contextlib.contextmanager
 def _on(device, stream):
-    """Makes `device` and `stream` (None: the device's current stream) the current ones, so that what the call
-    allocates belongs to the stream it is used on."""
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
-def _same_stream_device(stream, device):
+    """Makes `device` and `stream` (None: the device's current stream) the current ones, so that what a call
+    allocates belongs to the stream that it is used on."""
     if stream is not None and stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, not on {device} with the tensors")
+    with torch.cuda.device(device) if stream is None else torch.cuda.stream(stream):
+        yield
 
 
 def attn_kv4_write_raw(k_ptr, v_ptr, kc_ptr, ks_ptr, vc_ptr, vs_ptr, N, H, L, C, E, Ev, k_strides, v_strides, start,
@@ -470,13 +478,15 @@ def attn_kv4_write(cache, k: torch.Tensor, v: torch.Tensor, *, start: int = 0, p
         raise ValueError("the last dimension of k and v must be contiguous")
     _check_index("pos", pos, N, dev)
     _check_index("count", count, N, dev)
-    _same_stream_device(stream, dev)
     lib = load_library()
-    with _on(dev, stream):
-        st = lib.attn_kv4_write(k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in cache), N, H, k.shape[2], C, E, Ev,
-                                ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], _int32("start", start),
-                                None if pos is None else pos.data_ptr(), None if count is None else count.data_ptr(),
-                                DTYPES[k.dtype], torch.cuda.current_stream(dev).cuda_stream)
+    args = (k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in cache), N, H, k.shape[2], C, E, Ev, ks[0], ks[1], ks[2],
+            vs[0], vs[1], vs[2], _int32("start", start), None if pos is None else pos.data_ptr(),
+            None if count is None else count.data_ptr(), DTYPES[k.dtype])
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            st = lib.attn_kv4_write(*args, _stream_handle(dev))
+    else:
+        st = lib.attn_kv4_write(*args, _stream_handle(dev))
     _check(st)
 
 
@@ -492,20 +502,19 @@ def attn_kv4_read(cache, rows: int, *, start: int = 0, pos: torch.Tensor | None 
     """
     N, H, C, E, Ev = _cache_shape(cache)
     dev = cache[0].device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_kv4_read(cache, rows, start=start, pos=pos, kv_len=kv_len, dtype=dtype, k_out=k_out, v_out=v_out)
     if dtype not in DTYPES:
         raise ValueError("dtype must be bfloat16 or float32")
     rows = _int32("rows", rows)
     _check_index("pos", pos, N, dev)
     _check_index("kv_len", kv_len, N, dev)
-    _same_stream_device(stream, dev)
-    lib = load_library()
-    with _on(dev, stream):
-        k_out = _output("k_out", k_out, (N, H, rows, E), dtype, dev)
-        v_out = _output("v_out", v_out, (N, H, rows, Ev), dtype, dev)
-        st = lib.attn_kv4_read(*(t.data_ptr() for t in cache), k_out.data_ptr(), v_out.data_ptr(), N, H, rows, C, E, Ev,
-                               _int32("start", start), None if pos is None else pos.data_ptr(),
-                               None if kv_len is None else kv_len.data_ptr(), DTYPES[dtype],
-                               torch.cuda.current_stream(dev).cuda_stream)
+    k_out = _output("k_out", k_out, (N, H, rows, E), dtype, dev)
+    v_out = _output("v_out", v_out, (N, H, rows, Ev), dtype, dev)
+    st = load_library().attn_kv4_read(*(t.data_ptr() for t in cache), k_out.data_ptr(), v_out.data_ptr(), N, H, rows, C, E,
+                                      Ev, _int32("start", start), None if pos is None else pos.data_ptr(),
+                                      None if kv_len is None else kv_len.data_ptr(), DTYPES[dtype], _stream_handle(dev))
     _check(st)
     return k_out, v_out
 
@@ -556,7 +565,13 @@ def attn_decode_kv4(q: torch.Tensor, cache, *, scale: float, length: int | None 
     """
     _check_kinds(mode, mask_kind, keep_first)
     N, H, C, E, Ev = _cache_shape(cache)
-    dev = cache[0].device
+    kc, ks, vc, vs = cache
+    dev = kc.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_decode_kv4(q, cache, scale=scale, length=length, kv_len=kv_len, mode=mode, sink=sink,
+                                   mask_kind=mask_kind, window=window, keep_first=keep_first, out=out, lse=lse,
+                                   workspace=workspace)
     if q.dim() != 4 or q.dtype != torch.bfloat16 or q.device != dev or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous 4-D bfloat16 tensor on {dev} with the cache")
     Nq, Hq, L, Eq = q.shape
@@ -569,21 +584,15 @@ def attn_decode_kv4(q: torch.Tensor, cache, *, scale: float, length: int | None 
         raise ValueError(f"sink must be a contiguous float32 tensor of Hq values on {dev}")
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    _same_stream_device(stream, dev)
-    lib = load_library()
-    with _on(dev, stream):
-        out = _output("out", out, (N, Hq, L, Ev), torch.bfloat16, dev)
-        lse = _output("lse", lse, (N, Hq, L), torch.float32, dev)
-        handle = torch.cuda.current_stream(dev).cuda_stream
-        ws = _kv4_stream_workspace(dev, handle) if workspace is None else workspace
-        kind = "window" if mask_kind == "streaming" else mask_kind
-        kc, ks, vc, vs = cache
-        st = lib.attn_decode_kv4(q.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
-                                 out.data_ptr(), lse.data_ptr(), N, Hq, H, L, S, C, E, Ev, float(scale),
-                                 MODES[mode], None if sink is None else sink.data_ptr(), MASKS[kind],
-                                 _int32("window", window), _int32("keep_first", keep_first),
-                                 None if kv_len is None else kv_len.data_ptr(), ws.data_ptr(),
-                                 ws.numel() * ws.element_size(), handle)
+    out = torch.empty_like(q) if out is None and E == Ev else _output("out", out, (N, Hq, L, Ev), torch.bfloat16, dev)
+    lse = _output("lse", lse, (N, Hq, L), torch.float32, dev)
+    handle = _stream_handle(dev)
+    ws = _kv4_stream_workspace(dev, handle) if workspace is None else workspace
+    st = load_library().attn_decode_kv4(
+        q.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), out.data_ptr(), lse.data_ptr(), N, Hq,
+        H, L, S, C, E, Ev, float(scale), MODES[mode], None if sink is None else sink.data_ptr(),
+        MASKS["window" if mask_kind == "streaming" else mask_kind], _int32("window", window),
+        _int32("keep_first", keep_first), None if kv_len is None else kv_len.data_ptr(), ws.data_ptr(), ws.nbytes, handle)
     _check(st)
     return out, lse
 

@@ -28,6 +28,7 @@
 // the CTA whose count completes the unit merges them.  The counter wraps to zero with the last
 // count (atomicInc), so no launch has to clear it.
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -43,7 +44,7 @@ namespace attn {
 namespace {
 
 constexpr int KC = 128;         // keys per chunk
-constexpr int GW = 4;           // consumer warps per group; each takes 32 keys of the group's chunks
+constexpr int CONSUMERS = 8;    // consumer warps
 constexpr int NPROD = 2;        // producer warps (one thread each)
 constexpr int NMERGE = 2;       // merging warps
 constexpr int NQ = 4;           // units whose query rows may be on chip
@@ -77,16 +78,18 @@ struct Params {
 
 template <int E, int EV, int NT>
 struct Cfg {
-  // consumer groups: 16 warps in all leave 128 registers a thread, which 8 query rows fit into; 16 rows need 12 warps' 168
-  static constexpr int NG = NT == 1 ? 3 : 2;
-  static constexpr int NCW = NG * GW;
+  // A consumer warp works on MT 16-key tiles at once: 64 keys for 8 query rows, 32 for 16 (what 168 registers hold);
+  // the GW warps of a group share a chunk, the NG groups take chunks in turn.  More and narrower warps (12 of 32 keys)
+  // measured slower (16 x 131072 x 8 heads: 460 us against 421): a warp's fixed work per chunk is what they repeat.
+  static constexpr int MT = 4 / NT, GW = KC / (16 * MT), NG = CONSUMERS / GW;
+  static constexpr int NCW = CONSUMERS;
   static constexpr int WARPS = NCW + NPROD + NMERGE;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int K_CODES = KC * E / 2, V_CODES = KC * EV / 2;
   static constexpr int K_SCALES = KC * E / 16, V_SCALES = KC * EV / 16;
   static constexpr int OFF_V = K_CODES, OFF_KS = K_CODES + V_CODES, OFF_VS = OFF_KS + K_SCALES;
   static constexpr int STAGE = OFF_VS + V_SCALES;
-  static constexpr int NSTAGE = (NT == 1 ? 165888 : 147456) / STAGE;
+  static constexpr int NSTAGE = 147456 / STAGE / NG * NG;
   static_assert(NSTAGE % NG == 0, "each stage belongs to one consumer group, which waits its phases in order");
   static constexpr int MD = EV / 16;                              // 16-dimension tiles of O^T
   static constexpr int NX = NT * MD * 32;                         // float4 of one warp's O fragments
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
   constexpr int KS = E / 16;        // k-steps of K Q^T
   constexpr int KB = E / 8;         // bytes of a key that a lane reads
   constexpr int VB = EV / 16;       // bytes of a value row that a lane reads
-  constexpr int MT = 2;             // 16-key tiles of a warp's 32 keys
+  constexpr int MT = C::MT, GW = C::GW;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   Misc* misc = reinterpret_cast<Misc*>(smem + C::OFF_MISC);
@@ -581,7 +584,9 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
       for (int e = 0; e < 2; ++e) qi[t][e] = (2 * c4 + e + 8 * t) % p.L;
     uint32_t qf[NT][KS][2];
     float o[NT][MD][4];
-    float cq[NT][2], m_run[NT][2], l_run[NT][2];
+    // of the rows 2 c4, 2 c4 + 1: the logits' factor, P_SHIFT - running maximum (base 2), the raw logit above which
+    // the maximum moves (-inf while there is none), the sum
+    float cq[NT][2], bias[NT][2], limit[NT][2], l_run[NT][2];
     bool ok = true;
     unsigned idx = grp, s = grp, phase = 0;  // the group's next chunk, its stage (idx % NSTAGE) and the stage's parity
     const uint8_t* kp = smem + (j0 + kap_k) * (E / 2) + c4 * KB;  // this lane's bytes in stage 0
@@ -626,7 +631,8 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
           const float c = fminf(fmaxf(p.c_dot * down, 1e-37f), 3e38f);
           cq[t][0] = __shfl_sync(0xffffffffu, c, 8 * c4);
           cq[t][1] = __shfl_sync(0xffffffffu, c, 8 * c4 + 4);
-          m_run[t][0] = m_run[t][1] = -INFINITY;
+          bias[t][0] = bias[t][1] = P_SHIFT;
+          limit[t][0] = limit[t][1] = -INFINITY;
           l_run[t][0] = l_run[t][1] = 0.f;
 #pragma unroll
           for (int d = 0; d < MD; ++d) o[t][d][0] = o[t][d][1] = o[t][d][2] = o[t][d][3] = 0.f;
@@ -640,17 +646,24 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
       const int off = w.s.len - p.L;
       const int lo_first = windowed ? off - p.window + 1 : 0, lo_last = windowed ? off + p.L - p.window : 0;
       const int hi_first = causal ? off + 1 : w.s.len, hi_last = w.s.len;
-      // every row sees all of this warp's keys of a chunk if the first one is one of n_full from lo_last on
-      const unsigned n_full = static_cast<unsigned>(max(0, hi_first - 16 * MT - lo_last + 1));
+      // Every row sees all of this warp's keys of the chunk idx if full_first <= idx < full_first + n_full: those
+      // after the kept keys' whose first key is in [lo_last, hi_first - 16 MT].
+      const int c_first = (max(lo_last - j0, 0) + KC - 1) / KC, c_last = (hi_first - 16 * MT - j0) / KC;
+      const unsigned n_full = hi_first >= 16 * MT + j0 && c_last >= c_first ? c_last - c_first + 1 : 0;
+      const unsigned full_first = w.i0 - w.lo + static_cast<unsigned>(c_first - w.s.kb_win + w.s.nc_head);
 
       while (idx < i1) {
         ok = __all_sync(0xffffffffu, mbar_sleep(full_bar(s), phase));
         if (!ok) break;
         const unsigned at = s * C::STAGE;
-        const int key0 = w.key0(w.lo + (idx - w.i0)) + j0;
-        const bool full = static_cast<unsigned>(key0 - lo_last) < n_full;
-        // keys that no row sees need no work
-        if (full || (key0 < hi_last && (key0 + 16 * MT > lo_first || key0 < p.keep))) {
+        const bool full = idx - full_first < n_full;
+        int key0 = 0;  // needed for masks only
+        bool work = true;
+        if (!full) {  // keys that no row sees need no work
+          key0 = w.key0(w.lo + (idx - w.i0)) + j0;
+          work = key0 < hi_last && (key0 + 16 * MT > lo_first || key0 < p.keep);
+        }
+        if (work) {
           float sc[MT][NT][4];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -708,7 +721,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
               const int x = (16 * mt + 8 * z) * (EV / 16);
-              vs[mt][z] = vsp0[at + x] | (static_cast<uint32_t>(vsp1[at + x]) << 16);
+              vs[mt][z] = vsp0[at + x] * 0x80u + vsp1[at + x] * 0x800000u;
             }
           if (!full) {
             auto seen_by = [&](int key, int row_at) {
@@ -730,10 +743,10 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                   const int key = key0 + 16 * mt + (kap_v ^ x) + 8 * z;
-                  const uint32_t b = (vs[mt][z] >> (16 * x)) & 0xFFu;
+                  const uint32_t b = (vs[mt][z] >> (16 * x + 7)) & 0xFFu;
                   const bool seen = key < hi_last && (key >= lo_first || key < p.keep);
                   odd = odd || (seen && b > KV4_MAX_SCALE);
-                  if (seen && b <= KV4_MAX_SCALE) both |= b << (16 * x);
+                  if (seen && b <= KV4_MAX_SCALE) both |= b << (16 * x + 7);
                 }
                 vs[mt][z] = both;
               }
@@ -765,41 +778,39 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
               mx[t][e] = fmaxf(sc[0][t][e], sc[0][t][e + 2]);
 #pragma unroll
               for (int mt = 1; mt < MT; ++mt) mx[t][e] = fmax3(mx[t][e], sc[mt][t][e], sc[mt][t][e + 2]);
-              if constexpr (!RBF) mx[t][e] *= cq[t][e];
-              over = over || mx[t][e] > m_run[t][e] + RESCALE;
+              over = over || mx[t][e] > limit[t][e];
             }
           if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                float m = fmaxf(m_run[t][e], mx[t][e]);
+                float m = mx[t][e];
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                const float f = m > m_run[t][e] ? ex2(m_run[t][e] - m) : 1.f;
-                l_run[t][e] *= f;
+                if (m > limit[t][e]) {
+                  const float c = RBF ? 1.f : cq[t][e];
+                  const float f = limit[t][e] == -INFINITY ? 0.f : ex2(P_SHIFT - bias[t][e] - m * c);
+                  l_run[t][e] *= f;
 #pragma unroll
-                for (int d = 0; d < MD; ++d) {
-                  o[t][d][e] *= f;
-                  o[t][d][e + 2] *= f;
+                  for (int d = 0; d < MD; ++d) {
+                    o[t][d][e] *= f;
+                    o[t][d][e + 2] *= f;
+                  }
+                  bias[t][e] = P_SHIFT - m * c;
+                  limit[t][e] = m + RESCALE / c;
                 }
-                m_run[t][e] = m;
               }
           }
           uint32_t pt[MT][NT][2];
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            float bias[2], cc[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              cc[e] = RBF ? 1.f : cq[t][e];
-              bias[e] = P_SHIFT - (m_run[t][e] == -INFINITY ? 0.f : m_run[t][e]);
-            }
+            const float c0 = RBF ? 1.f : cq[t][0], c1 = RBF ? 1.f : cq[t][1];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              const float p0 = ex2(fmaf(sc[mt][t][0], cc[0], bias[0])), p1 = ex2(fmaf(sc[mt][t][1], cc[1], bias[1]));
-              const float p2 = ex2(fmaf(sc[mt][t][2], cc[0], bias[0])), p3 = ex2(fmaf(sc[mt][t][3], cc[1], bias[1]));
+              const float p0 = ex2(fmaf(sc[mt][t][0], c0, bias[t][0])), p1 = ex2(fmaf(sc[mt][t][1], c1, bias[t][1]));
+              const float p2 = ex2(fmaf(sc[mt][t][2], c0, bias[t][0])), p3 = ex2(fmaf(sc[mt][t][3], c1, bias[t][1]));
               l_run[t][0] += p0 + p2;
               l_run[t][1] += p1 + p3;
               pt[mt][t][0] = transpose8(pack_f16x2(p0, p1));
@@ -815,7 +826,6 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
               load_words<VB>(vp0 + at + (16 * mt + 8 * z) * (EV / 2), v[2 * z]);
               load_words<VB>(vp1 + at + (16 * mt + 8 * z) * (EV / 2), v[2 * z + 1]);
             }
-            const uint32_t sa = vs[mt][0] << 7, sz = vs[mt][1] << 7;
 #pragma unroll
             for (int x = 0; x < VB / 4; ++x) {
               // bytes with one dimension's elements of two keys: even dimensions, odd dimensions
@@ -826,7 +836,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
               kv4_unpack8(low_halves(v[2][x] >> 4, v[3][x]), oz);
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                const uint32_t a[4] = {hmul2(ea[y], sa), hmul2(oa[y], sa), hmul2(ez[y], sz), hmul2(oz[y], sz)};
+                const uint32_t a[4] = {hmul2(ea[y], vs[mt][0]), hmul2(oa[y], vs[mt][0]), hmul2(ez[y], vs[mt][1]), hmul2(oz[y], vs[mt][1])};
 #pragma unroll
                 for (int t = 0; t < NT; ++t) mma(o[t][4 * x + y], a, pt[mt][t][0], pt[mt][t][1]);
               }
@@ -857,7 +867,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
             l += __shfl_xor_sync(0xffffffffu, l, 4);
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
-            if (ra == 0) merge_ml[warp * 8 * NT + 8 * t + 2 * c4 + e] = make_float2(m_run[t][e], l);
+            if (ra == 0) merge_ml[warp * 8 * NT + 8 * t + 2 * c4 + e] = make_float2(limit[t][e] == -INFINITY ? -INFINITY : P_SHIFT - bias[t][e], l);
           }
 #pragma unroll
           for (int d = 0; d < MD; ++d)
@@ -935,9 +945,21 @@ template <int E, int EV, int NT, bool RBF>
 int launch_impl(const Params& p, unsigned G, cudaStream_t stream) {
   using C = Cfg<E, EV, NT>;
   auto kern = kv4_decode_kernel<E, EV, NT, RBF>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -13;
-  kern<<<G, C::THREADS, C::SMEM, stream>>>(p, G);
-  return cudaGetLastError() == cudaSuccess ? 0 : -13;
+  // the shared-memory limit is raised once per device; a launch that fails raises it again (the device was reset)
+  static std::atomic<bool> raised[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -13;
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    if (!raised[dev].load(std::memory_order_acquire)) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) break;
+      raised[dev].store(true, std::memory_order_release);
+    }
+    kern<<<G, C::THREADS, C::SMEM, stream>>>(p, G);
+    if (cudaGetLastError() == cudaSuccess) return 0;
+    raised[dev].store(false, std::memory_order_release);
+  }
+  cudaGetLastError();
+  return -13;
 }
 
 template <int E, int EV>
