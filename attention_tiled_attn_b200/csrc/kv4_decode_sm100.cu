@@ -49,7 +49,7 @@ constexpr int NPROD = 2;        // producer warps (one thread each)
 constexpr int NMERGE = 2;       // merging warps
 constexpr int NQ = 4;           // units whose query rows may be on chip
 constexpr int MAX_CTAS = 160;   // grid limit, which sizes the workspace
-constexpr int UNIT_COST = 1;    // a unit's beginning and end, in chunks, when the work is split
+constexpr int UNIT_COST = 2;    // a unit's beginning and end, in chunks, when the work is split
 constexpr int MIN_SHARE = 6;    // chunks of a CTA's share, at least
 constexpr int NO_SPLIT = 6;     // a unit of so many chunks is never split
 constexpr float RESCALE = 8.f;  // the running maximum follows the true one within 2^8
@@ -97,13 +97,13 @@ struct Cfg {
   static constexpr int OFF_MERGE = NSTAGE * STAGE;                // [NCW][NX] float4
   static constexpr int OFF_Q = OFF_MERGE + NCW * NX * 16;         // [NQ][8 NT][E] bf16
   static constexpr int OFF_ML = OFF_Q + NQ * Q_SLOT;              // [NCW][8 NT] float2
-  static constexpr int OFF_ROW = OFF_ML + NCW * 8 * NT * 8;       // [8 NT] float2: a row's merged (m, l)
-  static constexpr int OFF_BAR = OFF_ROW + 8 * NT * 8;
+  static constexpr int OFF_WT = OFF_ML + NCW * 8 * NT * 8;        // [NCW][8 NT] float: weights of the warps' states
+  static constexpr int OFF_BAR = OFF_WT + NCW * 8 * NT * 4;
   static constexpr int NBAR = 2 * NSTAGE + 2 * NQ + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;             // Misc
   static constexpr int SMEM = OFF_MISC + 128;
   // the merge of a unit's partials keeps its sums, then its weights, where the warps' fragments and the stages were
-  static constexpr int PARTS = THREADS / NX > 1 ? THREADS / NX : 1;
+  static constexpr int PARTS = 2 * THREADS / NX > 1 ? 2 * THREADS / NX : 1;
   static_assert(MAX_CTAS * 8 * NT * 4 <= NSTAGE * STAGE && PARTS <= NCW, "combine buffers");
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -294,23 +294,13 @@ __device__ __forceinline__ float row_factor(float M, float l, float s2, float* l
   return l == 0.f ? 0.f : f / l;
 }
 
-// Writes float4 x of a unit's O^T (rows 2 (x % 4) and + 1 of its row block, two dimensions) and, with
-// the first dimension, the rows' lse.  ml0, ml1: the two rows' (m, l).
+// Writes float4 x of a unit's O^T: rows 2 (x % 4) and + 1 of its row block, two dimensions.
 template <int EV, int MD>
-__device__ __forceinline__ void finish(const Params& p, size_t unit, int h, int x, float4 acc, float2 ml0, float2 ml1) {
-  const int lane = x & 31, d = (x >> 5) % MD, t = x / (32 * MD);
-  const int dim = (lane >> 2) * (EV / 8) + 2 * d;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = 8 * t + 2 * (lane & 3) + e;
-    if (r >= p.R) continue;
-    const size_t row = unit * p.R + r;
-    const float2 ml = e ? ml1 : ml0;
-    float lse;
-    const float f = row_factor(ml.x, ml.y, p.sink ? __ldg(p.sink + h * p.group + r / p.L) * LOG2E : -INFINITY, &lse);
-    *reinterpret_cast<uint32_t*>(p.out + row * EV + dim) = pack_bf16x2((e ? acc.y : acc.x) * f, (e ? acc.w : acc.z) * f);
-    if (dim == 0 && p.lse) p.lse[row] = lse;
-  }
+__device__ __forceinline__ void store_out(const Params& p, size_t unit, int x, float4 v) {
+  const int lane = x & 31, d = (x >> 5) % MD, r = 8 * (x / (32 * MD)) + 2 * (lane & 3);
+  __nv_bfloat16* dst = p.out + (unit * p.R + r) * EV + (lane >> 2) * (EV / 8) + 2 * d;
+  if (r < p.R) *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(v.x, v.z);
+  if (r + 1 < p.R) *reinterpret_cast<uint32_t*>(dst + EV) = pack_bf16x2(v.y, v.w);
 }
 
 template <int E, int EV, int NT, bool RBF>
@@ -327,7 +317,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
   volatile int* abort_flag = &misc->abort_flag;
   float4* merge = reinterpret_cast<float4*>(smem + C::OFF_MERGE);
   float2* merge_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-  float2* row_ml = reinterpret_cast<float2*>(smem + C::OFF_ROW);
+  float* wts = reinterpret_cast<float*>(smem + C::OFF_WT);
   auto full_bar = [&](unsigned s) -> uint32_t { return sb + C::OFF_BAR + 8u * s; };
   auto empty_bar = [&](unsigned s) -> uint32_t { return sb + C::OFF_BAR + 8u * (C::NSTAGE + s); };
   auto qfull_bar = [&](unsigned k) -> uint32_t { return sb + C::OFF_BAR + 8u * (2 * C::NSTAGE + k % NQ); };
@@ -335,20 +325,18 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
   const uint32_t mfull_bar = sb + C::OFF_BAR + 8u * (2 * C::NSTAGE + 2 * NQ), mempty_bar = mfull_bar + 8u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  if (tid < C::NBAR) {
+    const int x = tid;  // full, empty, qfull, qempty, mfull, mempty
+    mbar_init(sb + C::OFF_BAR + 8u * x, x < C::NSTAGE ? 1
+                                        : x < 2 * C::NSTAGE ? GW
+                                        : x < 2 * C::NSTAGE + NQ ? 1
+                                        : x < C::NBAR - 1 ? NCW
+                                                          : 1);
+    fence_barrier_init();
+  }
   if (tid == 0) {
     misc->abort_flag = 0;
     misc->n_pending = 0;
-    for (int s = 0; s < C::NSTAGE; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), GW);
-    }
-    for (int k = 0; k < NQ; ++k) {
-      mbar_init(qfull_bar(k), 1);
-      mbar_init(qempty_bar(k), NCW);
-    }
-    mbar_init(mfull_bar, NCW);
-    mbar_init(mempty_bar, 1);
-    fence_barrier_init();
   }
   // ---- this CTA's share of the work list ----
   Walk w;
@@ -452,56 +440,61 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
           : "memory");
       ok = both != 0;
       if (!ok) break;
-      // the groups that had a chunk of it
-      const int g0 = static_cast<int>(w.i0 % NG);
-      const int ng = static_cast<int>(min(w.hi - w.lo, static_cast<unsigned>(NG)));
+      // the warps that had a chunk of it: na from w0 on, cyclically
+      const int na = static_cast<int>(min(w.hi - w.lo, static_cast<unsigned>(NG))) * GW;
+      const int w0 = static_cast<int>(w.i0 % NG) * GW;
+      auto nth = [&](int y) { return w0 + y < NCW ? w0 + y : w0 + y - NCW; };
       const bool whole = w.whole();
       float* mine = p.partials + static_cast<size_t>(2 * blockIdx.x + (w.lo == 0 ? 1 : 0)) * (WS_SLOT / 4);
-      for (int x = mt; x < NX; x += NMERGE * 32) {
-        const int r = 8 * (x / (32 * MD)) + 2 * (x & 3);
+      // the weight of each warp's state in each row; of a whole unit's, with the row's final factor
+      for (int z = mt; z < na * 8 * NT; z += NMERGE * 32) {
+        const int r = z % (8 * NT), me = nth(z / (8 * NT));
         if (r >= p.R) continue;
-        float M0 = -INFINITY, M1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int g = 0; g < ng; ++g) {
-          const int w0 = (g0 + g < NG ? g0 + g : g0 + g - NG) * GW;
-          float2 e0[GW], e1[GW];
-          float4 v[GW];
-          float N0 = M0, N1 = M1;
+        float M = -INFINITY, l = 0.f;
+        for (int y = 0; y < na; ++y) M = fmaxf(M, merge_ml[nth(y) * 8 * NT + r].x);
+        for (int y = 0; y < na; ++y) {
+          const float2 e = merge_ml[nth(y) * 8 * NT + r];
+          l = fmaf(e.y, e.x == -INFINITY ? 0.f : ex2(e.x - M), l);
+        }
+        const float m = merge_ml[me * 8 * NT + r].x;
+        float wt = m == -INFINITY ? 0.f : ex2(m - M);
+        if (whole) {
+          float lse;
+          wt *= row_factor(M, l, p.sink ? __ldg(p.sink + w.h * p.group + r / p.L) * LOG2E : -INFINITY, &lse);
+          if (me == w0 && p.lse) p.lse[w.unit(p) * p.R + r] = lse;
+        } else if (me == w0) {
+          reinterpret_cast<float2*>(mine + MAX_ROWS * 128)[r] = make_float2(M, l);
+        }
+        wts[me * 8 * NT + r] = wt;
+      }
+      merge_bar();
 #pragma unroll
-          for (int y = 0; y < GW; ++y) {
-            e0[y] = merge_ml[(w0 + y) * 8 * NT + r];
-            e1[y] = merge_ml[(w0 + y) * 8 * NT + r + 1];
-            v[y] = merge[(w0 + y) * NX + x];
-            N0 = fmaxf(N0, e0[y].x);
-            N1 = fmaxf(N1, e1[y].x);
-          }
-          const float s0 = M0 == -INFINITY ? 0.f : ex2(M0 - N0), s1 = M1 == -INFINITY ? 0.f : ex2(M1 - N1);
-          acc = make_float4(acc.x * s0, acc.y * s1, acc.z * s0, acc.w * s1);
-          l0 *= s0;
-          l1 *= s1;
-          M0 = N0;
-          M1 = N1;
+      for (int t = 0; t < NT; ++t) {
+        const int r = 8 * t + 2 * (mt & 3);
+        if (r >= p.R) continue;
+        constexpr int PER = MD * 32 / (NMERGE * 32);  // float4 of a thread per row block
+        float4 acc[PER];
 #pragma unroll
-          for (int y = 0; y < GW; ++y) {
-            const float f0 = e0[y].x == -INFINITY ? 0.f : ex2(e0[y].x - M0);
-            const float f1 = e1[y].x == -INFINITY ? 0.f : ex2(e1[y].x - M1);
-            acc.x = fmaf(v[y].x, f0, acc.x);
-            acc.y = fmaf(v[y].y, f1, acc.y);
-            acc.z = fmaf(v[y].z, f0, acc.z);
-            acc.w = fmaf(v[y].w, f1, acc.w);
-            l0 = fmaf(e0[y].y, f0, l0);
-            l1 = fmaf(e1[y].y, f1, l1);
+        for (int i = 0; i < PER; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int y = 0; y < na; ++y) {
+          const int v0 = nth(y);
+          const float f0 = wts[v0 * 8 * NT + r], f1 = r + 1 < p.R ? wts[v0 * 8 * NT + r + 1] : 0.f;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const float4 v = merge[v0 * NX + t * MD * 32 + i * NMERGE * 32 + mt];
+            acc[i].x = fmaf(v.x, f0, acc[i].x);
+            acc[i].y = fmaf(v.y, f1, acc[i].y);
+            acc[i].z = fmaf(v.z, f0, acc[i].z);
+            acc[i].w = fmaf(v.w, f1, acc[i].w);
           }
         }
-        if (whole) {
-          finish<EV, MD>(p, w.unit(p), w.h, x, acc, make_float2(M0, l0), make_float2(M1, l1));
-        } else {
-          reinterpret_cast<float4*>(mine)[x] = acc;
-          if (((x >> 2) & 7) == 0 && ((x >> 5) % MD) == 0) {
-            float2* ml = reinterpret_cast<float2*>(mine + MAX_ROWS * 128);
-            ml[r] = make_float2(M0, l0);
-            ml[r + 1] = make_float2(M1, l1);
-          }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int x = t * MD * 32 + i * NMERGE * 32 + mt;
+          if (whole)
+            store_out<EV, MD>(p, w.unit(p), x, acc[i]);
+          else
+            reinterpret_cast<float4*>(mine)[x] = acc[i];
         }
       }
       if (!whole) __threadfence();
@@ -890,23 +883,33 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     const unsigned unit = misc->pending[x0];
     const unsigned b0 = split.cta_of(misc->pend_u0[x0] + UNIT_COST);
     const int nseg = static_cast<int>(split.cta_of(misc->pend_u0[x0] + UNIT_COST + misc->pend_nc[x0] - 1) - b0) + 1;
-    float* wts = reinterpret_cast<float*>(smem);  // [nseg][8 NT]
+    float* seg_wts = reinterpret_cast<float*>(smem);  // [nseg][8 NT]
     auto slot = [&](int y) { return p.partials + static_cast<size_t>(2 * (b0 + y) + (y == 0 ? 1 : 0)) * (WS_SLOT / 4); };
     for (int r = warp; r < p.R; r += C::WARPS) {
+      float2 e[(MAX_CTAS + 31) / 32];
       float M = -INFINITY, l = 0.f;
-      for (int y = lane; y < nseg; y += 32)
-        M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(slot(y) + MAX_ROWS * 128) + r).x);
+#pragma unroll
+      for (int i = 0; i < (MAX_CTAS + 31) / 32; ++i) {
+        const int y = 32 * i + lane;
+        e[i] = y < nseg ? __ldcg(reinterpret_cast<const float2*>(slot(y) + MAX_ROWS * 128) + r) : make_float2(-INFINITY, 0.f);
+        M = fmaxf(M, e[i].x);
+      }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-      for (int y = lane; y < nseg; y += 32) {
-        const float2 e = __ldcg(reinterpret_cast<const float2*>(slot(y) + MAX_ROWS * 128) + r);
-        const float f = e.x == -INFINITY ? 0.f : ex2(e.x - M);
-        wts[y * 8 * NT + r] = f;
-        l = fmaf(e.y, f, l);
+#pragma unroll
+      for (int i = 0; i < (MAX_CTAS + 31) / 32; ++i) {
+        e[i].x = e[i].x == -INFINITY ? 0.f : ex2(e[i].x - M);
+        l = fmaf(e[i].y, e[i].x, l);
       }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-      if (lane == 0) row_ml[r] = make_float2(M, l);
+      const int h = static_cast<int>(unit % p.H);
+      float lse;
+      const float f = row_factor(M, l, p.sink ? __ldg(p.sink + h * p.group + r / p.L) * LOG2E : -INFINITY, &lse);
+#pragma unroll
+      for (int i = 0; i < (MAX_CTAS + 31) / 32; ++i)
+        if (32 * i + lane < nseg) seg_wts[(32 * i + lane) * 8 * NT + r] = e[i].x * f;
+      if (lane == 0 && p.lse) p.lse[static_cast<size_t>(unit) * p.R + r] = lse;
     }
     __syncthreads();
     for (int z = tid; z < C::PARTS * NX; z += C::THREADS) {
@@ -914,10 +917,10 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
       if (r >= p.R) continue;
       const int r1 = r + 1 < p.R ? r + 1 : r;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 16
       for (int y = part; y < nseg; y += C::PARTS) {
         const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(y)) + x);
-        const float f0 = wts[y * 8 * NT + r], f1 = wts[y * 8 * NT + r1];
+        const float f0 = seg_wts[y * 8 * NT + r], f1 = seg_wts[y * 8 * NT + r1];
         acc.x = fmaf(v.x, f0, acc.x);
         acc.y = fmaf(v.y, f1, acc.y);
         acc.z = fmaf(v.z, f0, acc.z);
@@ -927,15 +930,14 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     }
     __syncthreads();
     for (int x = tid; x < NX; x += C::THREADS) {
-      const int r = 8 * (x / (32 * MD)) + 2 * (x & 3);
-      if (r >= p.R) continue;
+      if (8 * (x / (32 * MD)) + 2 * (x & 3) >= p.R) continue;
       float4 acc = merge[x];
 #pragma unroll
       for (int y = 1; y < C::PARTS; ++y) {
         const float4 v = merge[y * NX + x];
         acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
       }
-      finish<EV, MD>(p, unit, static_cast<int>(unit % p.H), x, acc, row_ml[r], row_ml[r + 1 < p.R ? r + 1 : r]);
+      store_out<EV, MD>(p, unit, x, acc);
     }
     __syncthreads();
   }
