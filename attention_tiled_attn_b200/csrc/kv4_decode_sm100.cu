@@ -802,10 +802,12 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
             const float c0 = RBF ? 1.f : cq[t][0], c1 = RBF ? 1.f : cq[t][1];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              const float p0 = ex2(fmaf(sc[mt][t][0], c0, bias[t][0])), p1 = ex2(fmaf(sc[mt][t][1], c1, bias[t][1]));
-              const float p2 = ex2(fmaf(sc[mt][t][2], c0, bias[t][0])), p3 = ex2(fmaf(sc[mt][t][3], c1, bias[t][1]));
-              l_run[t][0] += p0 + p2;
-              l_run[t][1] += p1 + p3;
+              float x0, x1, x2, x3;
+              fma2g(x0, x1, sc[mt][t][0], sc[mt][t][1], c0, c1, bias[t][0], bias[t][1]);
+              fma2g(x2, x3, sc[mt][t][2], sc[mt][t][3], c0, c1, bias[t][0], bias[t][1]);
+              const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
+              add2(l_run[t][0], l_run[t][1], p0, p1);
+              add2(l_run[t][0], l_run[t][1], p2, p3);
               pt[mt][t][0] = transpose8(pack_f16x2(p0, p1));
               pt[mt][t][1] = transpose8(pack_f16x2(p2, p3));
             }
@@ -917,14 +919,22 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
       if (r >= p.R) continue;
       const int r1 = r + 1 < p.R ? r + 1 : r;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 16
-      for (int y = part; y < nseg; y += C::PARTS) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(y)) + x);
-        const float f0 = seg_wts[y * 8 * NT + r], f1 = seg_wts[y * 8 * NT + r1];
-        acc.x = fmaf(v.x, f0, acc.x);
-        acc.y = fmaf(v.y, f1, acc.y);
-        acc.z = fmaf(v.z, f0, acc.z);
-        acc.w = fmaf(v.w, f1, acc.w);
+      for (int y0 = part; y0 < nseg; y0 += 16 * C::PARTS) {  // 16 loads in flight
+        float4 v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int y = y0 + i * C::PARTS;
+          v[i] = y < nseg ? __ldcg(reinterpret_cast<const float4*>(slot(y)) + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int y = min(y0 + i * C::PARTS, nseg - 1);
+          const float f0 = seg_wts[y * 8 * NT + r], f1 = seg_wts[y * 8 * NT + r1];
+          acc.x = fmaf(v[i].x, f0, acc.x);
+          acc.y = fmaf(v[i].y, f1, acc.y);
+          acc.z = fmaf(v[i].z, f0, acc.z);
+          acc.w = fmaf(v[i].w, f1, acc.w);
+        }
       }
       merge[z] = acc;
     }
