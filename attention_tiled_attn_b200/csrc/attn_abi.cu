@@ -343,7 +343,7 @@ int attn_kv4_write(const void* k, const void* v, void* k_codes, void* k_scales, 
   if (major != 10) return ATTN_ERR_DEVICE;
   const Kv4WriteArgs a{k,          v,          k_codes,    k_scales,   v_codes,    v_scales,   N,     H,   L,    C, E, Ev,
                        k_stride_n, k_stride_h, k_stride_l, v_stride_n, v_stride_h, v_stride_l, start, pos, count};
-  return launch_kv4_write(a, dtype == ATTN_BF16, static_cast<cudaStream_t>(stream_ptr));
+  return launch_kv4_write(a, dtype == ATTN_BF16, sms, static_cast<cudaStream_t>(stream_ptr));
 }
 
 int attn_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales, void* k, void* v,
@@ -356,7 +356,7 @@ int attn_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes
   if (device_info(&dev, &sms, &major) != ATTN_OK) return ATTN_ERR_CUDA;
   if (major != 10) return ATTN_ERR_DEVICE;
   const Kv4ReadArgs a{k_codes, k_scales, v_codes, v_scales, k, v, N, H, rows, C, E, Ev, start, pos, kv_len};
-  return launch_kv4_read(a, dtype == ATTN_BF16, static_cast<cudaStream_t>(stream_ptr));
+  return launch_kv4_read(a, dtype == ATTN_BF16, sms, static_cast<cudaStream_t>(stream_ptr));
 }
 
 int attn_decode_kv4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,

@@ -135,8 +135,8 @@ struct Kv4DecodeArgs {
   int mask_kind, window, keep;
   const int* kv_len;  // [N] or nullptr (S)
 };
-int launch_kv4_write(const Kv4WriteArgs& a, bool bf16, cudaStream_t stream);
-int launch_kv4_read(const Kv4ReadArgs& a, bool bf16, cudaStream_t stream);
+int launch_kv4_write(const Kv4WriteArgs& a, bool bf16, int num_sms, cudaStream_t stream);
+int launch_kv4_read(const Kv4ReadArgs& a, bool bf16, int num_sms, cudaStream_t stream);
 size_t kv4_decode_workspace_bytes();
 int launch_kv4_decode(const Kv4DecodeArgs& a, void* workspace, int num_sms, cudaStream_t stream);
 unsigned int take_status_kv4(cudaStream_t s);

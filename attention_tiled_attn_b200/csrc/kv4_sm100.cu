@@ -11,9 +11,10 @@
 // subtracting 768) falls on the right side.
 //
 // Both passes move every byte once: (E + Ev) values in (out) and 9/16 of a byte per value out
-// (in), so HBM bounds them.  One thread per block of 16: a thread moves 32 (bf16) or 64 (fp32)
-// consecutive bytes of values, 8 bytes of elements and one scale byte, and neighbouring
-// threads neighbouring ones, so every sector is used whole.
+// (in), so HBM bounds them.  A thread works on blocks of 16 values: 32 (bf16) or 64 (fp32)
+// bytes of values in 32-byte accesses, 8 bytes of elements and one scale byte, neighbouring
+// threads on neighbouring blocks, so that every 32-byte sector is moved whole.  It has BPT
+// blocks in flight, and a CTA finds its place in the tensors with one 64-bit division.
 
 #include <cstdint>
 #include <cuda.h>
@@ -23,16 +24,13 @@
 
 #include "kernels.h"
 #include "kv4.cuh"
+#include "ptx_sm100.cuh"
 
 namespace attn {
 
 namespace {
 
 constexpr int WT = 256;  // threads per CTA
-
-struct Vec16 {  // 16 values of one block
-  float x[16];
-};
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
@@ -56,144 +54,233 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
 }
 
-template <bool BF16>
-__device__ __forceinline__ void load16(const void* p, float (&x)[16]) {
-  if constexpr (BF16) {
-    const uint4* s = static_cast<const uint4*>(p);
-    const uint4 a = __ldg(s), b = __ldg(s + 1);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+// Blocks of 16 per thread: 4 keep enough bytes in flight (131072 x 8 rows read: 106 us, 6.5 TB/s, against 134 with 1);
+// where that would leave SMs without a CTA, 1 (one row of 32 x 8 heads written and read: 5.0 us against 8.5).
+constexpr int WIDE = 4;
+
+// 32 bytes, 32-byte aligned or (the caller's tensors may be) only 16-byte aligned
+__device__ __forceinline__ void load32(const void* p, bool wide, uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
   } else {
-    const float4* s = static_cast<const float4*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 a = __ldg(s + i);
-      x[4 * i] = a.x;
-      x[4 * i + 1] = a.y;
-      x[4 * i + 2] = a.z;
-      x[4 * i + 3] = a.w;
-    }
+    const uint4* s = static_cast<const uint4*>(p);
+    const uint4 a = s[0], b = s[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    uint4* d = static_cast<uint4*>(p);
+    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(WT) kv4_write_kernel(const Kv4WriteArgs a) {
-  long long t = static_cast<long long>(blockIdx.x) * WT + threadIdx.x;
-  const int kb = a.E / KV4_BLOCK, vb = a.Ev / KV4_BLOCK;
-  const long long rows = static_cast<long long>(a.N) * a.H * a.L;
-  const bool is_v = t >= rows * kb;
-  if (is_v) t -= rows * kb;
-  const int nb = is_v ? vb : kb;
-  if (t >= rows * nb) return;
-  const unsigned row = static_cast<unsigned>(t / nb);
-  const int b = static_cast<int>(t % nb);
-  const unsigned nh = row / a.L, l = row % a.L;
-  const unsigned n = nh / a.H, h = nh % a.H;
-  if (a.count && static_cast<int>(l) >= __ldg(a.count + n)) return;
-  const long long to = static_cast<long long>(a.pos ? __ldg(a.pos + n) : a.start) + l;
-  if (to < 0 || to >= a.C) return;
-  const size_t off = is_v ? n * a.v_sn + h * a.v_sh + l * a.v_sl : n * a.k_sn + h * a.k_sh + l * a.k_sl;
-  const char* src = static_cast<const char*>(is_v ? a.v : a.k) + (off + b * KV4_BLOCK) * (BF16 ? 2 : 4);
-  float x[16];
-  load16<BF16>(src, x);
-  float most = fabsf(x[0]);
-#pragma unroll
-  for (int i = 1; i < 16; ++i) most = max_nan(most, fabsf(x[i]));
-  const uint32_t byte = scale_byte(most);
-  uint2 codes = make_uint2(0u, 0u);
-  if (byte != 0 && byte != KV4_NAN_SCALE) {
-    const float s = scale_value(byte);
-    if constexpr (BF16) {
-      const float r = __frcp_rn(s);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __fsub_rn(__fmaf_rn(x[i], r, 768.f), 768.f);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], s);
-    }
-    codes.x = kv4_pack8(x);
-    codes.y = kv4_pack8(x + 8);
+// Where a CTA's tile (of TILE blocks) lies: K's tiles first, then V's; within a tensor the blocks of 16 run over (n, h, row, block).
+template <int TILE>
+struct Place {
+  bool v;
+  int shift;              // log2 of the blocks of a row
+  long long first, total; // first block of the tile, blocks of the tensor
+  unsigned nh0, r0;       // of the block at the start of the tile's first row
+  __device__ __forceinline__ Place(int E, int Ev, long long rows_all, int rows) {
+    const long long kt = ((rows_all << (E == 128 ? 3 : 2)) + TILE - 1) / TILE;
+    v = blockIdx.x >= kt;
+    shift = (v ? Ev : E) == 128 ? 3 : 2;
+    first = (static_cast<long long>(blockIdx.x) - (v ? kt : 0)) * TILE;
+    total = rows_all << shift;
+    const unsigned row = static_cast<unsigned>(first >> shift);
+    nh0 = row / rows;
+    r0 = row % rows;
   }
-  const size_t at = (static_cast<size_t>(nh) * a.C + to) * nb + b;
-  static_cast<uint2*>(is_v ? a.v_codes : a.k_codes)[at] = codes;
-  static_cast<uint8_t*>(is_v ? a.v_scales : a.k_scales)[at] = static_cast<uint8_t>(byte);
+  // (n, h) and row of the tile's block i; false behind the tensor's end
+  __device__ __forceinline__ bool at(int i, int rows, unsigned& nh, unsigned& r) const {
+    nh = nh0;
+    r = r0 + (static_cast<unsigned>(i) >> shift);
+    if (r >= static_cast<unsigned>(rows)) {  // past the unit's end (TILE blocks are at most TILE / 4 rows, so no overflow)
+      nh += r / rows;
+      r %= rows;
+    }
+    return first + i < total;
+  }
+};
+
+template <bool BF16, int BPT>
+__global__ void __launch_bounds__(WT) kv4_write_kernel(const Kv4WriteArgs a) {
+  const Place<WT * BPT> at(a.E, a.Ev, static_cast<long long>(a.N) * a.H * a.L, a.L);
+  const char* src = static_cast<const char*>(at.v ? a.v : a.k);
+  const size_t sn = at.v ? a.v_sn : a.k_sn, sh = at.v ? a.v_sh : a.k_sh, sl = at.v ? a.v_sl : a.k_sl;
+  const bool wide = ((reinterpret_cast<uintptr_t>(src) | (sn | sh | sl) * (BF16 ? 2 : 4)) & 31) == 0;
+  uint2* codes_out = static_cast<uint2*>(at.v ? a.v_codes : a.k_codes);
+  uint8_t* scales_out = static_cast<uint8_t*>(at.v ? a.v_scales : a.k_scales);
+  constexpr int WORDS = BF16 ? 1 : 2;  // of 32 bytes per block
+  uint32_t in[BPT][WORDS][8];
+  size_t to[BPT];
+  bool live[BPT];
+#pragma unroll
+  for (int i = 0; i < BPT; ++i) {
+    const int x = i * WT + threadIdx.x, b = x & ((1 << at.shift) - 1);
+    unsigned nh, l;
+    live[i] = at.at(x, a.L, nh, l);
+    if (!live[i]) continue;
+    const unsigned n = nh / a.H, h = nh - n * a.H;
+    const long long row = static_cast<long long>(a.pos ? __ldg(a.pos + n) : a.start) + l;
+    live[i] = row >= 0 && row < a.C && (!a.count || static_cast<int>(l) < __ldg(a.count + n));
+    if (!live[i]) continue;
+    to[i] = ((static_cast<size_t>(nh) * a.C + row) << at.shift) + b;
+    const char* p = src + (n * sn + h * sh + l * sl + b * KV4_BLOCK) * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int y = 0; y < WORDS; ++y) load32(p + 32 * y, wide, in[i][y]);
+  }
+#pragma unroll
+  for (int i = 0; i < BPT; ++i) {
+    if (!live[i]) continue;
+    float x[16];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      if constexpr (BF16) {
+        x[2 * y] = __uint_as_float(in[i][0][y] << 16);
+        x[2 * y + 1] = __uint_as_float(in[i][0][y] & 0xFFFF0000u);
+      } else {
+        x[y] = __uint_as_float(in[i][0][y]);
+        x[8 + y] = __uint_as_float(in[i][WORDS - 1][y]);
+      }
+    }
+    float most = max_nan(fabsf(x[0]), fabsf(x[1]));
+#pragma unroll
+    for (int y = 2; y < 16; ++y) most = max_nan(most, fabsf(x[y]));
+    const uint32_t byte = scale_byte(most);
+    uint2 codes = make_uint2(0u, 0u);
+    if (byte != 0 && byte != KV4_NAN_SCALE) {
+      const float s = scale_value(byte);
+      if constexpr (BF16) {
+        const float r = __frcp_rn(s);
+#pragma unroll
+        for (int y = 0; y < 16; y += 2) {
+          float u0, u1;
+          fma2g(u0, u1, x[y], x[y + 1], r, r, 768.f, 768.f);
+          fma2g(x[y], x[y + 1], u0, u1, 1.f, 1.f, -768.f, -768.f);
+        }
+      } else {
+#pragma unroll
+        for (int y = 0; y < 16; ++y) x[y] = __fdiv_rn(x[y], s);
+      }
+      codes.x = kv4_pack8(x);
+      codes.y = kv4_pack8(x + 8);
+    }
+    codes_out[to[i]] = codes;
+    scales_out[to[i]] = static_cast<uint8_t>(byte);
+  }
 }
 
 __device__ __forceinline__ uint32_t half2_to_bf162(uint32_t h) {  // exact for the values of the cache
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
-  return r;
+  return pack_bf16x2(f.x, f.y);
 }
 
-template <bool BF16>
+template <bool BF16, int BPT>
 __global__ void __launch_bounds__(WT) kv4_read_kernel(const Kv4ReadArgs a) {
-  long long t = static_cast<long long>(blockIdx.x) * WT + threadIdx.x;
-  const int kb = a.E / KV4_BLOCK, vb = a.Ev / KV4_BLOCK;
-  const long long rows = static_cast<long long>(a.N) * a.H * a.rows;
-  const bool is_v = t >= rows * kb;
-  if (is_v) t -= rows * kb;
-  const int nb = is_v ? vb : kb;
-  if (t >= rows * nb) return;
-  const unsigned row = static_cast<unsigned>(t / nb);
-  const int b = static_cast<int>(t % nb);
-  const unsigned nh = row / a.rows, r = row % a.rows;
-  const unsigned n = nh / a.H;
-  const long long from = static_cast<long long>(a.pos ? __ldg(a.pos + n) : a.start) + r;
-  const long long end = a.kv_len ? min(static_cast<long long>(__ldg(a.kv_len + n)), static_cast<long long>(a.C))
-                                 : static_cast<long long>(a.C);
-  uint32_t h[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-  if (from >= 0 && from < end) {
-    const size_t at = (static_cast<size_t>(nh) * a.C + from) * nb + b;
-    const uint2 codes = __ldg(static_cast<const uint2*>(is_v ? a.v_codes : a.k_codes) + at);
-    const uint32_t s2 = kv4_scale2(__ldg(static_cast<const uint8_t*>(is_v ? a.v_scales : a.k_scales) + at));
-    uint32_t c[4];
-    kv4_unpack8(codes.x, c);
+  const Place<WT * BPT> at(a.E, a.Ev, static_cast<long long>(a.N) * a.H * a.rows, a.rows);
+  char* dst = static_cast<char*>(at.v ? a.v : a.k);
+  const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+  const uint2* codes_in = static_cast<const uint2*>(at.v ? a.v_codes : a.k_codes);
+  const uint8_t* scales_in = static_cast<const uint8_t*>(at.v ? a.v_scales : a.k_scales);
+  uint2 codes[BPT];
+  uint32_t scale[BPT];
+  bool live[BPT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = hmul2(c[i], s2);
-    kv4_unpack8(codes.y, c);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[4 + i] = hmul2(c[i], s2);
+  for (int i = 0; i < BPT; ++i) {
+    const int x = i * WT + threadIdx.x;
+    unsigned nh, r;
+    live[i] = at.at(x, a.rows, nh, r);
+    codes[i] = make_uint2(0u, 0u);
+    scale[i] = 0u;
+    if (!live[i]) continue;
+    long long row = a.start, end = a.C;
+    if (a.pos || a.kv_len) {
+      const unsigned n = nh / a.H;
+      if (a.pos) row = __ldg(a.pos + n);
+      if (a.kv_len) end = min(static_cast<long long>(__ldg(a.kv_len + n)), end);
+    }
+    row += r;
+    if (row >= 0 && row < end) {
+      const size_t from = ((static_cast<size_t>(nh) * a.C + row) << at.shift) + (x & ((1 << at.shift) - 1));
+      codes[i] = __ldg(codes_in + from);
+      scale[i] = __ldg(scales_in + from);
+    }
   }
-  char* dst = static_cast<char*>(is_v ? a.v : a.k) + (static_cast<size_t>(row) * nb + b) * KV4_BLOCK * (BF16 ? 2 : 4);
-  if constexpr (BF16) {
-    uint4* d = reinterpret_cast<uint4*>(dst);
-    d[0] = make_uint4(half2_to_bf162(h[0]), half2_to_bf162(h[1]), half2_to_bf162(h[2]), half2_to_bf162(h[3]));
-    d[1] = make_uint4(half2_to_bf162(h[4]), half2_to_bf162(h[5]), half2_to_bf162(h[6]), half2_to_bf162(h[7]));
-  } else {
-    float4* d = reinterpret_cast<float4*>(dst);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i]));
-      const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i + 1]));
-      d[i] = make_float4(lo.x, lo.y, hi.x, hi.y);
+  for (int i = 0; i < BPT; ++i) {
+    if (!live[i]) continue;
+    const uint32_t s2 = kv4_scale2(scale[i]);
+    uint32_t h[8];
+    uint32_t c[4];
+    kv4_unpack8(codes[i].x, c);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) h[y] = hmul2(c[y], s2);
+    kv4_unpack8(codes[i].y, c);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) h[4 + y] = hmul2(c[y], s2);
+    char* p = dst + (at.first + i * WT + threadIdx.x) * KV4_BLOCK * (BF16 ? 2 : 4);
+    uint32_t w[8];
+    if constexpr (BF16) {
+#pragma unroll
+      for (int y = 0; y < 8; ++y) w[y] = half2_to_bf162(h[y]);
+      store32(p, wide, w);
+    } else {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[4 * z + y]));
+          w[2 * y] = __float_as_uint(f.x);
+          w[2 * y + 1] = __float_as_uint(f.y);
+        }
+        store32(p + 32 * z, wide, w);
+      }
     }
   }
 }
 
+unsigned tiles(int N, int H, int rows, int E, int Ev, int bpt) {
+  const long long all = static_cast<long long>(N) * H * rows, tile = WT * bpt;
+  return static_cast<unsigned>((all * (E / KV4_BLOCK) + tile - 1) / tile + (all * (Ev / KV4_BLOCK) + tile - 1) / tile);
+}
+// whether tiles of WIDE blocks per thread give every SM a few CTAs
+bool many(int N, int H, int rows, int E, int Ev, int num_sms) {
+  return tiles(N, H, rows, E, Ev, WIDE) >= 4u * static_cast<unsigned>(num_sms);
+}
+
+template <bool BF16, int BPT>
+void write_rows(const Kv4WriteArgs& a, cudaStream_t stream) {
+  kv4_write_kernel<BF16, BPT><<<tiles(a.N, a.H, a.L, a.E, a.Ev, BPT), WT, 0, stream>>>(a);
+}
+template <bool BF16, int BPT>
+void read_rows(const Kv4ReadArgs& a, cudaStream_t stream) {
+  kv4_read_kernel<BF16, BPT><<<tiles(a.N, a.H, a.rows, a.E, a.Ev, BPT), WT, 0, stream>>>(a);
+}
+
 }  // namespace
 
-int launch_kv4_write(const Kv4WriteArgs& a, bool bf16, cudaStream_t stream) {
-  const long long blocks = static_cast<long long>(a.N) * a.H * a.L * ((a.E + a.Ev) / KV4_BLOCK);
-  const unsigned grid = static_cast<unsigned>((blocks + WT - 1) / WT);
-  if (bf16)
-    kv4_write_kernel<true><<<grid, WT, 0, stream>>>(a);
+int launch_kv4_write(const Kv4WriteArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
+  if (many(a.N, a.H, a.L, a.E, a.Ev, num_sms))
+    bf16 ? write_rows<true, WIDE>(a, stream) : write_rows<false, WIDE>(a, stream);
   else
-    kv4_write_kernel<false><<<grid, WT, 0, stream>>>(a);
+    bf16 ? write_rows<true, 1>(a, stream) : write_rows<false, 1>(a, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -13;
 }
 
-int launch_kv4_read(const Kv4ReadArgs& a, bool bf16, cudaStream_t stream) {
-  const long long blocks = static_cast<long long>(a.N) * a.H * a.rows * ((a.E + a.Ev) / KV4_BLOCK);
-  const unsigned grid = static_cast<unsigned>((blocks + WT - 1) / WT);
-  if (bf16)
-    kv4_read_kernel<true><<<grid, WT, 0, stream>>>(a);
+int launch_kv4_read(const Kv4ReadArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
+  if (many(a.N, a.H, a.rows, a.E, a.Ev, num_sms))
+    bf16 ? read_rows<true, WIDE>(a, stream) : read_rows<false, WIDE>(a, stream);
   else
-    kv4_read_kernel<false><<<grid, WT, 0, stream>>>(a);
+    bf16 ? read_rows<true, 1>(a, stream) : read_rows<false, 1>(a, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -13;
 }
 
