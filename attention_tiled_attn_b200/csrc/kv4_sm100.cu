@@ -3,12 +3,14 @@
 // A block of 16 values x is stored as
 //   s = the 8-bit scale nearest to max|x| / 6 (ties to even, at most 10240)
 //   c = the 4-bit value nearest to x / s (ties to even, at most 6 in magnitude), 0 where s = 0
-// Both roundings are those of the exact quotients: the divisor 6 and the scale have mantissas
-// of at most 4 bits, so a correctly rounded fp32 quotient of an fp32 value lies on a midpoint
-// of the coarser grid only if the exact one does.  The bf16 path needs no division: x and a
-// midpoint times s both fit in 8 significant bits, so a quotient that is not a midpoint is at
-// least 2^-10 away from it, and x * (1 / s) rounded to a multiple of 2^-14 (by adding and
-// subtracting 768) falls on the right side.
+// Both roundings are those of the exact quotients.  The divisors 6 and s have mantissas of at most
+// 4 bits, so a correctly rounded fp32 quotient of an fp32 value lies on a midpoint of the coarser
+// grid only if the exact one does.  fp32 x: x / s from r = 1 / s (correctly rounded) by q = x r,
+// q + (x - q s) r, which is the correctly rounded quotient (Markstein's correction).  bf16 x needs
+// less: x and a midpoint times the divisor both fit in 8 significant bits, so a quotient that is
+// not a midpoint is at least 2^-9 of itself away from it, and a product with a reciprocal that is
+// off by 2^-22 falls on the right side once its last bits are rounded off: max|x| / 6 keeps 15
+// fraction bits, x / s a multiple of 2^-14 (by adding and subtracting 768).
 //
 // Both passes move every byte once: (E + Ev) values in (out) and 9/16 of a byte per value out
 // (in), so HBM bounds them.  A thread works on blocks of 16 values: 32 (bf16) or 64 (fp32)
@@ -38,16 +40,15 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// The scale byte of a block whose largest magnitude is `most`.
-__device__ __forceinline__ uint32_t scale_byte(float most) {
-  if (most != most) return KV4_NAN_SCALE;
-  const float y = __fdiv_rn(most, 6.f);
+// The scale byte of a block with max|x| / 6 = y (a NaN: the NaN mark).
+__device__ __forceinline__ uint32_t scale_byte(float y) {
   // below 2^-14 the scales are the multiples of 2^-17; above, 3 mantissa bits, and the fp32
   // exponent field less 127 - 15
   const uint32_t b = __float_as_uint(y);
   const uint32_t normal = ((b + 0x7FFFFu + ((b >> 20) & 1u)) >> 20) - (112u << 3);
   const uint32_t small = static_cast<uint32_t>(__float2int_rn(y * 131072.f));
-  return y < 6.103515625e-05f ? small : min(normal, KV4_MAX_SCALE);
+  const uint32_t byte = y < 6.103515625e-05f ? small : min(normal, KV4_MAX_SCALE);
+  return y != y ? KV4_NAN_SCALE : byte;
 }
 
 __device__ __forceinline__ float scale_value(uint32_t byte) {
@@ -82,99 +83,133 @@ __device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&w)[
   }
 }
 
-// Where a CTA's tile (of TILE blocks) lies: K's tiles first, then V's; within a tensor the blocks of 16 run over (n, h, row, block).
+// Where a CTA's tile (of TILE blocks) lies: K's tiles first, then V's; within a tensor the blocks of 16 run over
+// (n, h, row, block).  Most of a CTA's blocks are of one (n, h), which is divided out once.
 template <int TILE>
 struct Place {
   bool v;
   int shift;              // log2 of the blocks of a row
   long long first, total; // first block of the tile, blocks of the tensor
-  unsigned nh0, r0;       // of the block at the start of the tile's first row
-  __device__ __forceinline__ Place(int E, int Ev, long long rows_all, int rows) {
-    const long long kt = ((rows_all << (E == 128 ? 3 : 2)) + TILE - 1) / TILE;
+  unsigned n0, nh0, r0;   // of the tile's first row
+  __device__ __forceinline__ Place(int E, int Ev, int N, int H, int rows) {
+    const long long all = static_cast<long long>(N) * H * rows;
+    const long long kt = ((all << (E == 128 ? 3 : 2)) + TILE - 1) / TILE;
     v = blockIdx.x >= kt;
     shift = (v ? Ev : E) == 128 ? 3 : 2;
     first = (static_cast<long long>(blockIdx.x) - (v ? kt : 0)) * TILE;
-    total = rows_all << shift;
+    total = all << shift;
     const unsigned row = static_cast<unsigned>(first >> shift);
     nh0 = row / rows;
-    r0 = row % rows;
+    r0 = row - nh0 * rows;
+    n0 = nh0 / H;
   }
-  // (n, h) and row of the tile's block i; false behind the tensor's end
-  __device__ __forceinline__ bool at(int i, int rows, unsigned& nh, unsigned& r) const {
-    nh = nh0;
-    r = r0 + (static_cast<unsigned>(i) >> shift);
-    if (r >= static_cast<unsigned>(rows)) {  // past the unit's end (TILE blocks are at most TILE / 4 rows, so no overflow)
-      nh += r / rows;
-      r %= rows;
-    }
-    return first + i < total;
-  }
+  // the block within its row, and the row counted from row 0 of (n0, h0)
+  __device__ __forceinline__ int block(int i) const { return i & ((1 << shift) - 1); }
+  __device__ __forceinline__ unsigned row(int i) const { return r0 + (static_cast<unsigned>(i) >> shift); }
 };
+
+// q + (x - q s) r for two values, q = x r: the correctly rounded x / s where r is the correctly rounded 1 / s
+__device__ __forceinline__ void div2(float& q0, float& q1, float x0, float x1, float s, float r) {
+  float u0, u1, e0, e1;
+  fma2g(u0, u1, x0, x1, r, r, -0.f, -0.f);
+  fma2g(e0, e1, u0, u1, -s, -s, x0, x1);
+  fma2g(q0, q1, e0, e1, r, r, u0, u1);
+}
+
+// the larger magnitude of each half (its sign is of no use); a NaN stays one
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 
 template <bool BF16, int BPT>
 __global__ void __launch_bounds__(WT) kv4_write_kernel(const Kv4WriteArgs a) {
-  const Place<WT * BPT> at(a.E, a.Ev, static_cast<long long>(a.N) * a.H * a.L, a.L);
+  const Place<WT * BPT> at(a.E, a.Ev, a.N, a.H, a.L);
+  constexpr int SIZE = BF16 ? 2 : 4, WORDS = BF16 ? 1 : 2;  // bytes of a value, 32-byte pieces of a block
   const char* src = static_cast<const char*>(at.v ? a.v : a.k);
-  const size_t sn = at.v ? a.v_sn : a.k_sn, sh = at.v ? a.v_sh : a.k_sh, sl = at.v ? a.v_sl : a.k_sl;
-  const bool wide = ((reinterpret_cast<uintptr_t>(src) | (sn | sh | sl) * (BF16 ? 2 : 4)) & 31) == 0;
+  const size_t sn = (at.v ? a.v_sn : a.k_sn) * SIZE, sh = (at.v ? a.v_sh : a.k_sh) * SIZE, sl = (at.v ? a.v_sl : a.k_sl) * SIZE;
+  const bool wide = ((reinterpret_cast<uintptr_t>(src) | sn | sh | sl) & 31) == 0;
   uint2* codes_out = static_cast<uint2*>(at.v ? a.v_codes : a.k_codes);
   uint8_t* scales_out = static_cast<uint8_t*>(at.v ? a.v_scales : a.k_scales);
-  constexpr int WORDS = BF16 ? 1 : 2;  // of 32 bytes per block
+  // for the tile's first (n, h)
+  const char* src0 = src + at.n0 * sn + (at.nh0 - at.n0 * a.H) * sh;
+  const long long to0 = static_cast<long long>(at.nh0) * a.C;
+  const int pos0 = a.pos ? __ldg(a.pos + at.n0) : a.start, count0 = a.count ? __ldg(a.count + at.n0) : a.L;
+
   uint32_t in[BPT][WORDS][8];
-  size_t to[BPT];
-  bool live[BPT];
+  long long to[BPT];  // the block's place in the cache, or -1
 #pragma unroll
   for (int i = 0; i < BPT; ++i) {
-    const int x = i * WT + threadIdx.x, b = x & ((1 << at.shift) - 1);
-    unsigned nh, l;
-    live[i] = at.at(x, a.L, nh, l);
-    if (!live[i]) continue;
-    const unsigned n = nh / a.H, h = nh - n * a.H;
-    const long long row = static_cast<long long>(a.pos ? __ldg(a.pos + n) : a.start) + l;
-    live[i] = row >= 0 && row < a.C && (!a.count || static_cast<int>(l) < __ldg(a.count + n));
-    if (!live[i]) continue;
-    to[i] = ((static_cast<size_t>(nh) * a.C + row) << at.shift) + b;
-    const char* p = src + (n * sn + h * sh + l * sl + b * KV4_BLOCK) * (BF16 ? 2 : 4);
+    const int x = i * WT + threadIdx.x;
+    unsigned l = at.row(x);
+    const char* p = src0;
+    long long unit = to0;
+    int pos = pos0, count = count0;
+    to[i] = -1;
+    if (at.first + x >= at.total) continue;
+    if (l >= static_cast<unsigned>(a.L)) {  // past the end of the tile's first (n, h)
+      const unsigned q = l / a.L, nh = at.nh0 + q, n = nh / a.H;
+      l -= q * a.L;
+      p = src + n * sn + (nh - n * a.H) * sh;
+      unit = static_cast<long long>(nh) * a.C;
+      if (a.pos) pos = __ldg(a.pos + n);
+      if (a.count) count = __ldg(a.count + n);
+    }
+    const long long row = static_cast<long long>(pos) + l;
+    if (row < 0 || row >= a.C || static_cast<int>(l) >= count) continue;
+    to[i] = ((unit + row) << at.shift) + at.block(x);
+    p += l * sl + at.block(x) * (KV4_BLOCK * SIZE);
 #pragma unroll
     for (int y = 0; y < WORDS; ++y) load32(p + 32 * y, wide, in[i][y]);
   }
 #pragma unroll
   for (int i = 0; i < BPT; ++i) {
-    if (!live[i]) continue;
-    float x[16];
+    if (to[i] < 0) continue;
+    float x[16], y6;
+    if constexpr (BF16) {
+      uint32_t (&w)[8] = in[i][0];
+      const uint32_t m4 = max_abs2(max_abs2(max_abs2(w[0], w[1]), max_abs2(w[2], w[3])), max_abs2(max_abs2(w[4], w[5]), max_abs2(w[6], w[7])));
+      const float most = max_nan(__uint_as_float((m4 & 0x7FFFu) << 16), __uint_as_float(m4 & 0x7FFF0000u));
+      y6 = __uint_as_float((__float_as_uint(most * (1.f / 6.f)) + 0x80u) & 0xFFFFFF00u);
+      if (most != most) y6 = most;
 #pragma unroll
-    for (int y = 0; y < 8; ++y) {
-      if constexpr (BF16) {
-        x[2 * y] = __uint_as_float(in[i][0][y] << 16);
-        x[2 * y + 1] = __uint_as_float(in[i][0][y] & 0xFFFF0000u);
-      } else {
+      for (int y = 0; y < 8; ++y) {
+        x[2 * y] = __uint_as_float(w[y] << 16);
+        x[2 * y + 1] = __uint_as_float(w[y] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
         x[y] = __uint_as_float(in[i][0][y]);
         x[8 + y] = __uint_as_float(in[i][WORDS - 1][y]);
       }
+      float most = max_nan(fabsf(x[0]), fabsf(x[1]));
+#pragma unroll
+      for (int y = 2; y < 16; ++y) most = max_nan(most, fabsf(x[y]));
+      y6 = __fdiv_rn(most, 6.f);
     }
-    float most = max_nan(fabsf(x[0]), fabsf(x[1]));
+    const uint32_t byte = scale_byte(y6);
+    const float s = scale_value(byte);
+    if constexpr (BF16) {
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
 #pragma unroll
-    for (int y = 2; y < 16; ++y) most = max_nan(most, fabsf(x[y]));
-    const uint32_t byte = scale_byte(most);
-    uint2 codes = make_uint2(0u, 0u);
-    if (byte != 0 && byte != KV4_NAN_SCALE) {
-      const float s = scale_value(byte);
-      if constexpr (BF16) {
-        const float r = __frcp_rn(s);
-#pragma unroll
-        for (int y = 0; y < 16; y += 2) {
-          float u0, u1;
-          fma2g(u0, u1, x[y], x[y + 1], r, r, 768.f, 768.f);
-          fma2g(x[y], x[y + 1], u0, u1, 1.f, 1.f, -768.f, -768.f);
-        }
-      } else {
-#pragma unroll
-        for (int y = 0; y < 16; ++y) x[y] = __fdiv_rn(x[y], s);
+      for (int y = 0; y < 16; y += 2) {
+        float u0, u1;
+        fma2g(u0, u1, x[y], x[y + 1], r, r, 768.f, 768.f);
+        fma2g(x[y], x[y + 1], u0, u1, 1.f, 1.f, -768.f, -768.f);
       }
-      codes.x = kv4_pack8(x);
-      codes.y = kv4_pack8(x + 8);
+    } else if (byte < KV4_MAX_SCALE) {
+      const float r = __frcp_rn(s);
+#pragma unroll
+      for (int y = 0; y < 16; y += 2) div2(x[y], x[y + 1], x[y], x[y + 1], s, r);
+    } else {  // values that may be far above the scale, infinite or NaN
+#pragma unroll
+      for (int y = 0; y < 16; ++y) x[y] = __fdiv_rn(x[y], s);
     }
-    codes_out[to[i]] = codes;
+    const bool none = byte == 0 || byte == KV4_NAN_SCALE;
+    codes_out[to[i]] = make_uint2(none ? 0u : kv4_pack8(x), none ? 0u : kv4_pack8(x + 8));
     scales_out[to[i]] = static_cast<uint8_t>(byte);
   }
 }
@@ -186,31 +221,37 @@ __device__ __forceinline__ uint32_t half2_to_bf162(uint32_t h) {  // exact for t
 
 template <bool BF16, int BPT>
 __global__ void __launch_bounds__(WT) kv4_read_kernel(const Kv4ReadArgs a) {
-  const Place<WT * BPT> at(a.E, a.Ev, static_cast<long long>(a.N) * a.H * a.rows, a.rows);
+  const Place<WT * BPT> at(a.E, a.Ev, a.N, a.H, a.rows);
   char* dst = static_cast<char*>(at.v ? a.v : a.k);
   const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
   const uint2* codes_in = static_cast<const uint2*>(at.v ? a.v_codes : a.k_codes);
   const uint8_t* scales_in = static_cast<const uint8_t*>(at.v ? a.v_scales : a.k_scales);
+  // for the tile's first (n, h)
+  const long long from0 = static_cast<long long>(at.nh0) * a.C;
+  const int pos0 = a.pos ? __ldg(a.pos + at.n0) : a.start, end0 = a.kv_len ? min(__ldg(a.kv_len + at.n0), a.C) : a.C;
   uint2 codes[BPT];
   uint32_t scale[BPT];
   bool live[BPT];
 #pragma unroll
   for (int i = 0; i < BPT; ++i) {
     const int x = i * WT + threadIdx.x;
-    unsigned nh, r;
-    live[i] = at.at(x, a.rows, nh, r);
+    unsigned r = at.row(x);
+    long long unit = from0;
+    int pos = pos0, end = end0;
+    live[i] = at.first + x < at.total;
     codes[i] = make_uint2(0u, 0u);
     scale[i] = 0u;
     if (!live[i]) continue;
-    long long row = a.start, end = a.C;
-    if (a.pos || a.kv_len) {
-      const unsigned n = nh / a.H;
-      if (a.pos) row = __ldg(a.pos + n);
-      if (a.kv_len) end = min(static_cast<long long>(__ldg(a.kv_len + n)), end);
+    if (r >= static_cast<unsigned>(a.rows)) {  // past the end of the tile's first (n, h)
+      const unsigned q = r / a.rows, nh = at.nh0 + q;
+      r -= q * a.rows;
+      unit = static_cast<long long>(nh) * a.C;
+      if (a.pos) pos = __ldg(a.pos + nh / a.H);
+      if (a.kv_len) end = min(__ldg(a.kv_len + nh / a.H), a.C);
     }
-    row += r;
+    const long long row = static_cast<long long>(pos) + r;
     if (row >= 0 && row < end) {
-      const size_t from = ((static_cast<size_t>(nh) * a.C + row) << at.shift) + (x & ((1 << at.shift) - 1));
+      const long long from = ((unit + row) << at.shift) + at.block(x);
       codes[i] = __ldg(codes_in + from);
       scale[i] = __ldg(scales_in + from);
     }
