@@ -16,7 +16,7 @@
 // (in), so HBM bounds them.  A thread works on blocks of 16 values: 32 (bf16) or 64 (fp32)
 // bytes of values in 32-byte accesses, 8 bytes of elements and one scale byte, neighbouring
 // threads on neighbouring blocks, so that every 32-byte sector is moved whole.  It has BPT
-// blocks in flight, and a CTA finds its place in the tensors with one 64-bit division.
+// blocks in flight, and a CTA finds its place in the tensors once.
 
 #include <cstdint>
 #include <cuda.h>
@@ -32,7 +32,7 @@ namespace attn {
 
 namespace {
 
-constexpr int WT = 256;  // threads per CTA
+constexpr int WT = 128;  // threads per CTA
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
@@ -55,9 +55,12 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
 }
 
-// Blocks of 16 per thread: 4 keep enough bytes in flight (131072 x 8 rows read: 106 us, 6.5 TB/s, against 134 with 1);
-// where that would leave SMs without a CTA, 1 (one row of 32 x 8 heads written and read: 5.0 us against 8.5).
-constexpr int WIDE = 4;
+// Blocks of 16 per thread.  64 bytes of values in flight per thread and small CTAs measured best: bf16 2 blocks (4 x
+// 8192 x 8 rows of 128 + 128 written in 32 us; 1 block 37, 4 blocks of 256 threads 40; 131072 x 8 rows read in 105 us,
+// 6.5 TB/s; 1 block 113), fp32 1 block (written in 45 us; 2 blocks 49).  bf16 calls whose tiles of 2 would leave SMs
+// without a CTA take 1.
+template <bool BF16>
+constexpr int WIDE = BF16 ? 2 : 1;
 
 // 32 bytes, 32-byte aligned or (the caller's tensors may be) only 16-byte aligned
 __device__ __forceinline__ void load32(const void* p, bool wide, uint32_t (&w)[8]) {
@@ -293,9 +296,9 @@ unsigned tiles(int N, int H, int rows, int E, int Ev, int bpt) {
   const long long all = static_cast<long long>(N) * H * rows, tile = WT * bpt;
   return static_cast<unsigned>((all * (E / KV4_BLOCK) + tile - 1) / tile + (all * (Ev / KV4_BLOCK) + tile - 1) / tile);
 }
-// whether tiles of WIDE blocks per thread give every SM a few CTAs
+// whether tiles of 2 blocks per thread give every SM a few CTAs
 bool many(int N, int H, int rows, int E, int Ev, int num_sms) {
-  return tiles(N, H, rows, E, Ev, WIDE) >= 4u * static_cast<unsigned>(num_sms);
+  return tiles(N, H, rows, E, Ev, 2) >= 4u * static_cast<unsigned>(num_sms);
 }
 
 template <bool BF16, int BPT>
@@ -310,18 +313,22 @@ void read_rows(const Kv4ReadArgs& a, cudaStream_t stream) {
 }  // namespace
 
 int launch_kv4_write(const Kv4WriteArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
-  if (many(a.N, a.H, a.L, a.E, a.Ev, num_sms))
-    bf16 ? write_rows<true, WIDE>(a, stream) : write_rows<false, WIDE>(a, stream);
+  if (!bf16)
+    write_rows<false, WIDE<false>>(a, stream);
+  else if (many(a.N, a.H, a.L, a.E, a.Ev, num_sms))
+    write_rows<true, WIDE<true>>(a, stream);
   else
-    bf16 ? write_rows<true, 1>(a, stream) : write_rows<false, 1>(a, stream);
+    write_rows<true, 1>(a, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -13;
 }
 
 int launch_kv4_read(const Kv4ReadArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
-  if (many(a.N, a.H, a.rows, a.E, a.Ev, num_sms))
-    bf16 ? read_rows<true, WIDE>(a, stream) : read_rows<false, WIDE>(a, stream);
+  if (!bf16)
+    read_rows<false, WIDE<false>>(a, stream);
+  else if (many(a.N, a.H, a.rows, a.E, a.Ev, num_sms))
+    read_rows<true, WIDE<true>>(a, stream);
   else
-    bf16 ? read_rows<true, 1>(a, stream) : read_rows<false, 1>(a, stream);
+    read_rows<true, 1>(a, stream);
   return cudaGetLastError() == cudaSuccess ? 0 : -13;
 }
 
