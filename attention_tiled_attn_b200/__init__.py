@@ -372,19 +372,18 @@ def kv4_cache(N: int, H: int, capacity: int, E: int, Ev: int | None = None, devi
 
 
 def _cache_shape(cache):
-    """Checks a 4-bit cache's tensors and returns (N, H, capacity, E, Ev)."""
+    """Checks a 4-bit cache's tensors and returns (N, H, capacity, E, Ev, device)."""
     kc, ks, vc, vs = cache
     N, H, C, half = kc.shape
     half_v = vc.shape[3]
-    lead = (N, H, C)
-    if (tuple(ks.shape) != lead + (half // 8,) or tuple(vc.shape) != lead + (half_v,)
-            or tuple(vs.shape) != lead + (half_v // 8,)):
+    if ks.shape != (N, H, C, half // 8) or vc.shape != (N, H, C, half_v) or vs.shape != (N, H, C, half_v // 8):
         raise ValueError("the cache's tensors must be (N, H, C, E/2), (N, H, C, E/16), (N, H, C, Ev/2), (N, H, C, Ev/16)")
     dev = kc.device
-    for t in (kc, ks, vc, vs):
-        if t.dtype != torch.uint8 or not t.is_cuda or t.device != dev or not t.is_contiguous():
-            raise ValueError("the cache must be contiguous uint8 CUDA tensors on one device")
-    return N, H, C, 2 * half, 2 * half_v
+    if not (kc.is_cuda and ks.device == dev and vc.device == dev and vs.device == dev
+            and kc.dtype is ks.dtype is vc.dtype is vs.dtype is torch.uint8
+            and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("the cache must be contiguous uint8 CUDA tensors on one device")
+    return N, H, C, 2 * half, 2 * half_v, dev
 
 
 def _check_index(name: str, t, N: int, device):
@@ -393,11 +392,15 @@ def _check_index(name: str, t, N: int, device):
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape ({N},) on {device}")
 
 
-def _int32(name: str, x) -> int:
-    x = int(x)
-    if not -2**31 <= x < 2**31:
-        raise ValueError(f"{name} must fit in 32 bits")
-    return x
+def _int32(**values):
+    """The C interface takes 32-bit sizes: a larger value is rejected, not cut."""
+    for name, x in values.items():
+        if not -2**31 <= x < 2**31:
+            raise ValueError(f"{name} must fit in 32 bits")
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -463,25 +466,24 @@ def attn_kv4_write(cache, k: torch.Tensor, v: torch.Tensor, *, start: int = 0, p
     (pos (N,) int32 CUDA), or start + l without pos; with count (N,) int32 only
     its first count[n] rows are written.  Rows outside the cache are not written.
     """
-    N, H, C, E, Ev = _cache_shape(cache)
-    dev = cache[0].device
-    if k.dim() != 4 or v.dim() != 4 or k.shape[:2] != (N, H) or v.shape[:3] != k.shape[:3]:
-        raise ValueError("k and v must be (N, H, L, E) and (N, H, L, Ev) with the cache's N and H")
-    if k.shape[3] != E or v.shape[3] != Ev:
-        raise ValueError("k or v has another head dimension than the cache")
-    if k.dtype not in DTYPES or v.dtype != k.dtype:
+    N, H, C, E, Ev, dev = _cache_shape(cache)
+    ks, vs = k.shape, v.shape
+    if len(ks) != 4 or ks[:2] != (N, H) or vs != (N, H, ks[2], Ev) or ks[3] != E:
+        raise ValueError("k and v must be (N, H, L, E) and (N, H, L, Ev) with the cache's N, H, E and Ev")
+    if k.dtype not in DTYPES or v.dtype is not k.dtype:
         raise ValueError("k, v must share dtype bfloat16 or float32")
     if k.device != dev or v.device != dev:
         raise ValueError(f"k and v must be on {dev} with the cache")
-    ks, vs = k.stride(), v.stride()
-    if ks[3] != 1 or vs[3] != 1:
+    kst, vst = k.stride(), v.stride()
+    if kst[3] != 1 or vst[3] != 1:
         raise ValueError("the last dimension of k and v must be contiguous")
     _check_index("pos", pos, N, dev)
     _check_index("count", count, N, dev)
+    _int32(start=start)
+    kc, ksc, vc, vsc = cache
+    args = (k.data_ptr(), v.data_ptr(), kc.data_ptr(), ksc.data_ptr(), vc.data_ptr(), vsc.data_ptr(), N, H, ks[2], C, E, Ev,
+            kst[0], kst[1], kst[2], vst[0], vst[1], vst[2], start, _address(pos), _address(count), DTYPES[k.dtype])
     lib = load_library()
-    args = (k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in cache), N, H, k.shape[2], C, E, Ev, ks[0], ks[1], ks[2],
-            vs[0], vs[1], vs[2], _int32("start", start), None if pos is None else pos.data_ptr(),
-            None if count is None else count.data_ptr(), DTYPES[k.dtype])
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             st = lib.attn_kv4_write(*args, _stream_handle(dev))
@@ -500,22 +502,21 @@ def attn_kv4_read(cache, rows: int, *, start: int = 0, pos: torch.Tensor | None 
     Rows at or after kv_len[n] ((N,) int32 CUDA) and rows outside the cache come
     back as 0.  k_out and v_out may be given (contiguous, of `dtype`).
     """
-    N, H, C, E, Ev = _cache_shape(cache)
-    dev = cache[0].device
+    N, H, C, E, Ev, dev = _cache_shape(cache)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return attn_kv4_read(cache, rows, start=start, pos=pos, kv_len=kv_len, dtype=dtype, k_out=k_out, v_out=v_out)
     if dtype not in DTYPES:
         raise ValueError("dtype must be bfloat16 or float32")
-    rows = _int32("rows", rows)
+    _int32(rows=rows, start=start)
     _check_index("pos", pos, N, dev)
     _check_index("kv_len", kv_len, N, dev)
     k_out = _output("k_out", k_out, (N, H, rows, E), dtype, dev)
     v_out = _output("v_out", v_out, (N, H, rows, Ev), dtype, dev)
-    st = load_library().attn_kv4_read(*(t.data_ptr() for t in cache), k_out.data_ptr(), v_out.data_ptr(), N, H, rows, C, E,
-                                      Ev, _int32("start", start), None if pos is None else pos.data_ptr(),
-                                      None if kv_len is None else kv_len.data_ptr(), DTYPES[dtype], _stream_handle(dev))
-    _check(st)
+    kc, ks, vc, vs = cache
+    _check(load_library().attn_kv4_read(
+        kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), N, H, rows, C, E, Ev,
+        start, _address(pos), _address(kv_len), DTYPES[dtype], _stream_handle(dev)))
     return k_out, v_out
 
 
@@ -564,22 +565,21 @@ def attn_decode_kv4(q: torch.Tensor, cache, *, scale: float, length: int | None 
     of its own for a captured call).
     """
     _check_kinds(mode, mask_kind, keep_first)
-    N, H, C, E, Ev = _cache_shape(cache)
-    kc, ks, vc, vs = cache
-    dev = kc.device
+    N, H, C, E, Ev, dev = _cache_shape(cache)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return attn_decode_kv4(q, cache, scale=scale, length=length, kv_len=kv_len, mode=mode, sink=sink,
                                    mask_kind=mask_kind, window=window, keep_first=keep_first, out=out, lse=lse,
                                    workspace=workspace)
-    if q.dim() != 4 or q.dtype != torch.bfloat16 or q.device != dev or not q.is_contiguous():
+    if q.dim() != 4 or q.dtype is not torch.bfloat16 or q.device != dev or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous 4-D bfloat16 tensor on {dev} with the cache")
     Nq, Hq, L, Eq = q.shape
     if Nq != N or Eq != E:
         raise ValueError("q has another batch or head dimension than the cache")
-    S = C if length is None else _int32("length", length)
+    S = C if length is None else length
+    _int32(length=S, window=window, keep_first=keep_first)
     _check_index("kv_len", kv_len, N, dev)
-    if sink is not None and (sink.dtype != torch.float32 or sink.numel() != Hq or sink.device != dev
+    if sink is not None and (sink.dtype is not torch.float32 or sink.numel() != Hq or sink.device != dev
                              or not sink.is_contiguous()):
         raise ValueError(f"sink must be a contiguous float32 tensor of Hq values on {dev}")
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
@@ -588,12 +588,11 @@ def attn_decode_kv4(q: torch.Tensor, cache, *, scale: float, length: int | None 
     lse = _output("lse", lse, (N, Hq, L), torch.float32, dev)
     handle = _stream_handle(dev)
     ws = _kv4_stream_workspace(dev, handle) if workspace is None else workspace
-    st = load_library().attn_decode_kv4(
+    kc, ks, vc, vs = cache
+    _check(load_library().attn_decode_kv4(
         q.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), out.data_ptr(), lse.data_ptr(), N, Hq,
-        H, L, S, C, E, Ev, float(scale), MODES[mode], None if sink is None else sink.data_ptr(),
-        MASKS["window" if mask_kind == "streaming" else mask_kind], _int32("window", window),
-        _int32("keep_first", keep_first), None if kv_len is None else kv_len.data_ptr(), ws.data_ptr(), ws.nbytes, handle)
-    _check(st)
+        H, L, S, C, E, Ev, scale, MODES[mode], _address(sink), MASKS["window" if mask_kind == "streaming" else mask_kind],
+        window, keep_first, _address(kv_len), ws.data_ptr(), ws.nbytes, handle))
     return out, lse
 
 
