@@ -49,8 +49,8 @@ constexpr int NPROD = 2;        // producer warps (one thread each)
 constexpr int NMERGE = 2;       // merging warps
 constexpr int NQ = 4;           // units whose query rows may be on chip
 constexpr int MAX_CTAS = 160;   // grid limit, which sizes the workspace
-constexpr int UNIT_COST = 2;    // a unit's beginning and end, in chunks, when the work is split
-constexpr int MIN_SHARE = 6;    // chunks of a CTA's share, at least
+constexpr int UNIT_COST = 4;    // a unit's beginning and end, in chunks, when the work is split
+constexpr int MIN_SHARE = 4;    // chunks of a CTA's share, at least
 constexpr int NO_SPLIT = 6;     // a unit of so many chunks is never split
 constexpr float RESCALE = 8.f;  // the running maximum follows the true one within 2^8
 constexpr float P_SHIFT = 7.f;  // P is held times 2^7
@@ -885,8 +885,48 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     const unsigned unit = misc->pending[x0];
     const unsigned b0 = split.cta_of(misc->pend_u0[x0] + UNIT_COST);
     const int nseg = static_cast<int>(split.cta_of(misc->pend_u0[x0] + UNIT_COST + misc->pend_nc[x0] - 1) - b0) + 1;
-    float* seg_wts = reinterpret_cast<float*>(smem);  // [nseg][8 NT]
     auto slot = [&](int y) { return p.partials + static_cast<size_t>(2 * (b0 + y) + (y == 0 ? 1 : 0)) * (WS_SLOT / 4); };
+    const int h = static_cast<int>(unit % p.H);
+    constexpr int FEW = 4;
+    if (nseg <= FEW) {  // each thread finds its two rows' weights itself: one round of loads
+      for (int x = tid; x < NX; x += C::THREADS) {
+        const int r = 8 * (x / (32 * MD)) + 2 * (x & 3);
+        if (r >= p.R) continue;
+        float4 v[FEW];
+        float4 e[FEW];  // (m, l) of rows r and r + 1
+#pragma unroll
+        for (int y = 0; y < FEW; ++y) {
+          const float* src = slot(y < nseg ? y : 0);
+          v[y] = __ldcg(reinterpret_cast<const float4*>(src) + x);
+          e[y] = __ldcg(reinterpret_cast<const float4*>(src + MAX_ROWS * 128 + 2 * r));
+          if (y >= nseg) e[y] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f), v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float M0 = e[0].x, M1 = e[0].z, l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int y = 1; y < FEW; ++y) {
+          M0 = fmaxf(M0, e[y].x);
+          M1 = fmaxf(M1, e[y].z);
+        }
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int y = 0; y < FEW; ++y) {
+          const float f0 = e[y].x == -INFINITY ? 0.f : ex2(e[y].x - M0), f1 = e[y].z == -INFINITY ? 0.f : ex2(e[y].z - M1);
+          l0 = fmaf(e[y].y, f0, l0);
+          l1 = fmaf(e[y].w, f1, l1);
+          acc = make_float4(fmaf(v[y].x, f0, acc.x), fmaf(v[y].y, f1, acc.y), fmaf(v[y].z, f0, acc.z), fmaf(v[y].w, f1, acc.w));
+        }
+        float lse0, lse1;
+        const float f0 = row_factor(M0, l0, p.sink ? __ldg(p.sink + h * p.group + r / p.L) * LOG2E : -INFINITY, &lse0);
+        const float f1 = r + 1 < p.R ? row_factor(M1, l1, p.sink ? __ldg(p.sink + h * p.group + (r + 1) / p.L) * LOG2E : -INFINITY, &lse1) : 0.f;
+        store_out<EV, MD>(p, unit, x, make_float4(acc.x * f0, acc.y * f1, acc.z * f0, acc.w * f1));
+        if ((x & 28) == 0 && (x >> 5) % MD == 0 && p.lse) {
+          p.lse[static_cast<size_t>(unit) * p.R + r] = lse0;
+          if (r + 1 < p.R) p.lse[static_cast<size_t>(unit) * p.R + r + 1] = lse1;
+        }
+      }
+      continue;
+    }
+    float* seg_wts = reinterpret_cast<float*>(smem);  // [nseg][8 NT]
     for (int r = warp; r < p.R; r += C::WARPS) {
       float2 e[(MAX_CTAS + 31) / 32];
       float M = -INFINITY, l = 0.f;
@@ -905,7 +945,6 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
       }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-      const int h = static_cast<int>(unit % p.H);
       float lse;
       const float f = row_factor(M, l, p.sink ? __ldg(p.sink + h * p.group + r / p.L) * LOG2E : -INFINITY, &lse);
 #pragma unroll
