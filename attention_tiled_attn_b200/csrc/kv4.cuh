@@ -14,6 +14,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda_runtime.h>
 
 namespace attn {
 
@@ -49,6 +50,28 @@ __device__ __forceinline__ uint32_t kv4_pack8(const float* x) {
 
 // the fp16 pair (s, s) of a scale byte
 __device__ __forceinline__ uint32_t kv4_scale2(uint32_t byte) { return byte * 0x00800080u; }  // byte << 7 in both halves
+
+// Programmatic dependent launch.  The launches below let a kernel start while the one before it in the stream is still
+// running (the next kernel's start, set-up and scheduling then overlap it); no memory of the caller's is touched
+// before overlap_wait(), which returns once all earlier work of the stream is complete and visible.
+__device__ __forceinline__ void overlap_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void overlap_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_overlapped(void (*kern)(KArgs...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+                              Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;

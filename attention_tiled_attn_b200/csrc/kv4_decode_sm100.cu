@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
   const uint32_t mfull_bar = sb + C::OFF_BAR + 8u * (2 * C::NSTAGE + 2 * NQ), mempty_bar = mfull_bar + 8u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  overlap_start();
   if (tid < C::NBAR) {
     const int x = tid;  // full, empty, qfull, qempty, mfull, mempty
     mbar_init(sb + C::OFF_BAR + 8u * x, x < C::NSTAGE ? 1
@@ -338,6 +339,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     misc->abort_flag = 0;
     misc->n_pending = 0;
   }
+  overlap_wait();
   // ---- this CTA's share of the work list ----
   Walk w;
   unsigned T;
@@ -1005,11 +1007,10 @@ int launch_impl(const Params& p, unsigned G, cudaStream_t stream) {
       if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) break;
       raised[dev].store(true, std::memory_order_release);
     }
-    kern<<<G, C::THREADS, C::SMEM, stream>>>(p, G);
-    if (cudaGetLastError() == cudaSuccess) return 0;
+    if (launch_overlapped(kern, G, C::THREADS, C::SMEM, stream, p, G) == cudaSuccess) return 0;
+    cudaGetLastError();
     raised[dev].store(false, std::memory_order_release);
   }
-  cudaGetLastError();
   return -13;
 }
 

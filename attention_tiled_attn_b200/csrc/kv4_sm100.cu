@@ -128,6 +128,7 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
 
 template <bool BF16, int BPT>
 __global__ void __launch_bounds__(WT) kv4_write_kernel(const Kv4WriteArgs a) {
+  overlap_start();
   const Place<WT * BPT> at(a.E, a.Ev, a.N, a.H, a.L);
   constexpr int SIZE = BF16 ? 2 : 4, WORDS = BF16 ? 1 : 2;  // bytes of a value, 32-byte pieces of a block
   const char* src = static_cast<const char*>(at.v ? a.v : a.k);
@@ -135,6 +136,7 @@ __global__ void __launch_bounds__(WT) kv4_write_kernel(const Kv4WriteArgs a) {
   const bool wide = ((reinterpret_cast<uintptr_t>(src) | sn | sh | sl) & 31) == 0;
   uint2* codes_out = static_cast<uint2*>(at.v ? a.v_codes : a.k_codes);
   uint8_t* scales_out = static_cast<uint8_t*>(at.v ? a.v_scales : a.k_scales);
+  overlap_wait();
   // for the tile's first (n, h)
   const char* src0 = src + at.n0 * sn + (at.nh0 - at.n0 * a.H) * sh;
   const long long to0 = static_cast<long long>(at.nh0) * a.C;
@@ -224,11 +226,13 @@ __device__ __forceinline__ uint32_t half2_to_bf162(uint32_t h) {  // exact for t
 
 template <bool BF16, int BPT>
 __global__ void __launch_bounds__(WT) kv4_read_kernel(const Kv4ReadArgs a) {
+  overlap_start();
   const Place<WT * BPT> at(a.E, a.Ev, a.N, a.H, a.rows);
   char* dst = static_cast<char*>(at.v ? a.v : a.k);
   const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
   const uint2* codes_in = static_cast<const uint2*>(at.v ? a.v_codes : a.k_codes);
   const uint8_t* scales_in = static_cast<const uint8_t*>(at.v ? a.v_scales : a.k_scales);
+  overlap_wait();
   // for the tile's first (n, h)
   const long long from0 = static_cast<long long>(at.nh0) * a.C;
   const int pos0 = a.pos ? __ldg(a.pos + at.n0) : a.start, end0 = a.kv_len ? min(__ldg(a.kv_len + at.n0), a.C) : a.C;
@@ -302,34 +306,28 @@ bool many(int N, int H, int rows, int E, int Ev, int num_sms) {
 }
 
 template <bool BF16, int BPT>
-void write_rows(const Kv4WriteArgs& a, cudaStream_t stream) {
-  kv4_write_kernel<BF16, BPT><<<tiles(a.N, a.H, a.L, a.E, a.Ev, BPT), WT, 0, stream>>>(a);
+cudaError_t write_rows(const Kv4WriteArgs& a, cudaStream_t stream) {
+  return launch_overlapped(kv4_write_kernel<BF16, BPT>, tiles(a.N, a.H, a.L, a.E, a.Ev, BPT), WT, 0, stream, a);
 }
 template <bool BF16, int BPT>
-void read_rows(const Kv4ReadArgs& a, cudaStream_t stream) {
-  kv4_read_kernel<BF16, BPT><<<tiles(a.N, a.H, a.rows, a.E, a.Ev, BPT), WT, 0, stream>>>(a);
+cudaError_t read_rows(const Kv4ReadArgs& a, cudaStream_t stream) {
+  return launch_overlapped(kv4_read_kernel<BF16, BPT>, tiles(a.N, a.H, a.rows, a.E, a.Ev, BPT), WT, 0, stream, a);
 }
 
 }  // namespace
 
 int launch_kv4_write(const Kv4WriteArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
-  if (!bf16)
-    write_rows<false, WIDE<false>>(a, stream);
-  else if (many(a.N, a.H, a.L, a.E, a.Ev, num_sms))
-    write_rows<true, WIDE<true>>(a, stream);
-  else
-    write_rows<true, 1>(a, stream);
-  return cudaGetLastError() == cudaSuccess ? 0 : -13;
+  const cudaError_t e = !bf16                                           ? write_rows<false, WIDE<false>>(a, stream)
+                        : many(a.N, a.H, a.L, a.E, a.Ev, num_sms) ? write_rows<true, WIDE<true>>(a, stream)
+                                                                        : write_rows<true, 1>(a, stream);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 0 : -13;
 }
 
 int launch_kv4_read(const Kv4ReadArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
-  if (!bf16)
-    read_rows<false, WIDE<false>>(a, stream);
-  else if (many(a.N, a.H, a.rows, a.E, a.Ev, num_sms))
-    read_rows<true, WIDE<true>>(a, stream);
-  else
-    read_rows<true, 1>(a, stream);
-  return cudaGetLastError() == cudaSuccess ? 0 : -13;
+  const cudaError_t e = !bf16                                              ? read_rows<false, WIDE<false>>(a, stream)
+                        : many(a.N, a.H, a.rows, a.E, a.Ev, num_sms) ? read_rows<true, WIDE<true>>(a, stream)
+                                                                           : read_rows<true, 1>(a, stream);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 0 : -13;
 }
 
 }  // namespace attn
