@@ -94,12 +94,13 @@ struct Cfg {
   static constexpr int MD = EV / 16;                              // 16-dimension tiles of O^T
   static constexpr int NX = NT * MD * 32;                         // float4 of one warp's O fragments
   static constexpr int Q_SLOT = 8 * NT * E * 2;
-  static constexpr int OFF_MERGE = NSTAGE * STAGE;                // [NCW][NX] float4
-  static constexpr int OFF_Q = OFF_MERGE + NCW * NX * 16;         // [NQ][8 NT][E] bf16
-  static constexpr int OFF_ML = OFF_Q + NQ * Q_SLOT;              // [NCW][8 NT] float2
-  static constexpr int OFF_WT = OFF_ML + NCW * 8 * NT * 8;        // [NCW][8 NT] float: weights of the warps' states
+  static constexpr int NBUF = NT == 1 ? 2 : 1;                    // units whose states may wait for the merging warps
+  static constexpr int OFF_MERGE = NSTAGE * STAGE;                // [NBUF][NCW][NX] float4
+  static constexpr int OFF_Q = OFF_MERGE + NBUF * NCW * NX * 16;  // [NQ][8 NT][E] bf16
+  static constexpr int OFF_ML = OFF_Q + NQ * Q_SLOT;              // [NBUF][NCW][8 NT] float2
+  static constexpr int OFF_WT = OFF_ML + NBUF * NCW * 8 * NT * 8; // [NCW][8 NT] float: weights of the warps' states
   static constexpr int OFF_BAR = OFF_WT + NCW * 8 * NT * 4;
-  static constexpr int NBAR = 2 * NSTAGE + 2 * NQ + 2;
+  static constexpr int NBAR = 2 * NSTAGE + 2 * NQ + 2 * NBUF;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;             // Misc
   static constexpr int SMEM = OFF_MISC + 128;
   // the merge of a unit's partials keeps its sums, then its weights, where the warps' fragments and the stages were
@@ -322,7 +323,8 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
   auto empty_bar = [&](unsigned s) -> uint32_t { return sb + C::OFF_BAR + 8u * (C::NSTAGE + s); };
   auto qfull_bar = [&](unsigned k) -> uint32_t { return sb + C::OFF_BAR + 8u * (2 * C::NSTAGE + k % NQ); };
   auto qempty_bar = [&](unsigned k) -> uint32_t { return sb + C::OFF_BAR + 8u * (2 * C::NSTAGE + NQ + k % NQ); };
-  const uint32_t mfull_bar = sb + C::OFF_BAR + 8u * (2 * C::NSTAGE + 2 * NQ), mempty_bar = mfull_bar + 8u;
+  auto mfull_bar = [&](unsigned k) -> uint32_t { return sb + C::OFF_BAR + 8u * (2 * C::NSTAGE + 2 * NQ + k % C::NBUF); };
+  auto mempty_bar = [&](unsigned k) -> uint32_t { return mfull_bar(k) + 8u * C::NBUF; };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   overlap_start();
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     mbar_init(sb + C::OFF_BAR + 8u * x, x < C::NSTAGE ? 1
                                         : x < 2 * C::NSTAGE ? GW
                                         : x < 2 * C::NSTAGE + NQ ? 1
-                                        : x < C::NBAR - 1 ? NCW
+                                        : x < C::NBAR - C::NBUF ? NCW
                                                           : 1);
     fence_barrier_init();
   }
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     misc->abort_flag = 0;
     misc->n_pending = 0;
   }
-  overlap_wait();
+  if (p.kv_len != nullptr) overlap_wait();  // else only the sizes decide the shares
   // ---- this CTA's share of the work list ----
   Walk w;
   unsigned T;
@@ -358,7 +360,10 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     T *= p.H;
   }
   const unsigned Ge = min(G, (T + MIN_SHARE - 1) / MIN_SHARE);
-  if (blockIdx.x >= Ge) return;
+  if (blockIdx.x >= Ge) {
+    overlap_wait();
+    return;
+  }
   const Split split(T, Ge);
   unsigned at[2] = {split.start(blockIdx.x), split.start(blockIdx.x + 1)};
   if (p.kv_len != nullptr) {
@@ -422,6 +427,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     }
   }
   bool more = w.first(p);
+  if (p.kv_len == nullptr) overlap_wait();
   __syncthreads();
 
   if (warp >= NCW + NPROD) {
@@ -429,7 +435,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     const int mt = tid - (NCW + NPROD) * 32;
     bool ok = true;
     for (; more; more = w.next(p)) {
-      ok = mbar_sleep(mfull_bar, w.k & 1);
+      ok = mbar_sleep(mfull_bar(w.k), (w.k / C::NBUF) & 1);
       // both warps decide together
       uint32_t both;
       asm volatile(
@@ -448,17 +454,22 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
       auto nth = [&](int y) { return w0 + y < NCW ? w0 + y : w0 + y - NCW; };
       const bool whole = w.whole();
       float* mine = p.partials + static_cast<size_t>(2 * blockIdx.x + (w.lo == 0 ? 1 : 0)) * (WS_SLOT / 4);
+      const float4* buf = merge + (w.k % C::NBUF) * NCW * NX;
+      const float2* buf_ml = merge_ml + (w.k % C::NBUF) * NCW * 8 * NT;
       // the weight of each warp's state in each row; of a whole unit's, with the row's final factor
       for (int z = mt; z < na * 8 * NT; z += NMERGE * 32) {
         const int r = z % (8 * NT), me = nth(z / (8 * NT));
         if (r >= p.R) continue;
+        float2 e[NCW];
         float M = -INFINITY, l = 0.f;
-        for (int y = 0; y < na; ++y) M = fmaxf(M, merge_ml[nth(y) * 8 * NT + r].x);
-        for (int y = 0; y < na; ++y) {
-          const float2 e = merge_ml[nth(y) * 8 * NT + r];
-          l = fmaf(e.y, e.x == -INFINITY ? 0.f : ex2(e.x - M), l);
+#pragma unroll
+        for (int y = 0; y < NCW; ++y) {
+          e[y] = y < na ? buf_ml[nth(y) * 8 * NT + r] : make_float2(-INFINITY, 0.f);
+          M = fmaxf(M, e[y].x);
         }
-        const float m = merge_ml[me * 8 * NT + r].x;
+#pragma unroll
+        for (int y = 0; y < NCW; ++y) l = fmaf(e[y].y, e[y].x == -INFINITY ? 0.f : ex2(e[y].x - M), l);
+        const float m = buf_ml[me * 8 * NT + r].x;
         float wt = m == -INFINITY ? 0.f : ex2(m - M);
         if (whole) {
           float lse;
@@ -478,16 +489,19 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
         float4 acc[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int y = 0; y < na; ++y) {
-          const int v0 = nth(y);
-          const float f0 = wts[v0 * 8 * NT + r], f1 = r + 1 < p.R ? wts[v0 * 8 * NT + r + 1] : 0.f;
+        for (int y0 = 0; y0 < na; y0 += GW) {
 #pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const float4 v = merge[v0 * NX + t * MD * 32 + i * NMERGE * 32 + mt];
-            acc[i].x = fmaf(v.x, f0, acc[i].x);
-            acc[i].y = fmaf(v.y, f1, acc[i].y);
-            acc[i].z = fmaf(v.z, f0, acc[i].z);
-            acc[i].w = fmaf(v.w, f1, acc[i].w);
+          for (int y = 0; y < GW; ++y) {
+            const int v0 = nth(y0) + y;
+            const float f0 = wts[v0 * 8 * NT + r], f1 = r + 1 < p.R ? wts[v0 * 8 * NT + r + 1] : 0.f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+              const float4 v = buf[v0 * NX + t * MD * 32 + i * NMERGE * 32 + mt];
+              acc[i].x = fmaf(v.x, f0, acc[i].x);
+              acc[i].y = fmaf(v.y, f1, acc[i].y);
+              acc[i].z = fmaf(v.z, f0, acc[i].z);
+              acc[i].w = fmaf(v.w, f1, acc[i].w);
+            }
           }
         }
 #pragma unroll
@@ -502,7 +516,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
       if (!whole) __threadfence();
       merge_bar();
       if (mt == 0) {
-        mbar_arrive(mempty_bar);
+        mbar_arrive(mempty_bar(w.k));
         if (!whole) {
           const unsigned b0 = split.cta_of(w.u0 + UNIT_COST), b1 = split.cta_of(w.u0 + UNIT_COST + w.s.nc - 1);
           if (atomicInc(p.counters + b0, b1 - b0) == b1 - b0) {
@@ -850,11 +864,11 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
         }
       }
       if (!ok) break;
-      // hand the state to the merging warps, once they have read the last one
-      if (w.k > 0) {
-        ok = __all_sync(0xffffffffu, mbar_sleep(mempty_bar, (w.k - 1) & 1));
-        if (!ok) break;
-      }
+      // hand the state to the merging warps, once they have read what the buffer holds
+      ok = __all_sync(0xffffffffu, mbar_sleep(mempty_bar(w.k), ((w.k / C::NBUF) & 1) ^ 1));
+      if (!ok) break;
+      float4* const my_o = merge + (w.k % C::NBUF) * NCW * NX + warp * NX + lane;
+      float2* const my_ml = merge_ml + ((w.k % C::NBUF) * NCW + warp) * 8 * NT + 2 * c4;
       if (mine) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -864,15 +878,15 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
             l += __shfl_xor_sync(0xffffffffu, l, 4);
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
-            if (ra == 0) merge_ml[warp * 8 * NT + 8 * t + 2 * c4 + e] = make_float2(limit[t][e] == -INFINITY ? -INFINITY : P_SHIFT - bias[t][e], l);
+            if (ra == 0) my_ml[8 * t + e] = make_float2(limit[t][e] == -INFINITY ? -INFINITY : P_SHIFT - bias[t][e], l);
           }
 #pragma unroll
           for (int d = 0; d < MD; ++d)
-            merge[warp * NX + (t * MD + d) * 32 + lane] = make_float4(o[t][d][0], o[t][d][1], o[t][d][2], o[t][d][3]);
+            my_o[(t * MD + d) * 32] = make_float4(o[t][d][0], o[t][d][1], o[t][d][2], o[t][d][3]);
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(mfull_bar);
+      if (lane == 0) mbar_arrive(mfull_bar(w.k));
     }
     if (!ok) *abort_flag = 1;
   }
