@@ -528,12 +528,15 @@ def _output(name, t, shape, dtype, device):
     return t
 
 
+KV4_WORKSPACE_ZERO = 4096  # leading bytes of a workspace that are zero before its first use
 _kv4_workspaces: dict = {}  # (device index, stream handle) -> workspace
 
 
 def kv4_workspace(device="cuda") -> torch.Tensor:
-    """A workspace for attn_decode_kv4, ready for use on the current stream (zeroed there)."""
-    return torch.zeros(load_library().attn_decode_kv4_workspace_bytes(), dtype=torch.uint8, device=device)
+    """A workspace for attn_decode_kv4, ready for use on the current stream (its counters are zeroed there)."""
+    ws = torch.empty(load_library().attn_decode_kv4_workspace_bytes(), dtype=torch.uint8, device=device)
+    ws[:KV4_WORKSPACE_ZERO].zero_()
+    return ws
 
 
 def _kv4_stream_workspace(device, handle):

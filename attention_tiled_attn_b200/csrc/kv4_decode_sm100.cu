@@ -35,6 +35,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "attn_b200.h"
 #include "kernels.h"
 #include "kv4.cuh"
 #include "ptx_sm100.cuh"
@@ -54,7 +55,7 @@ constexpr int MIN_SHARE = 4;    // chunks of a CTA's share, at least
 constexpr int NO_SPLIT = 6;     // a unit of so many chunks is never split
 constexpr float RESCALE = 8.f;  // the running maximum follows the true one within 2^8
 constexpr float P_SHIFT = 7.f;  // P is held times 2^7
-constexpr size_t WS_HEAD = 4096;  // arrival counters, one per CTA
+constexpr size_t WS_HEAD = ATTN_DECODE_KV4_WORKSPACE_ZERO;  // arrival counters, one per CTA
 constexpr int MAX_ROWS = 16;
 constexpr size_t WS_SLOT = MAX_ROWS * (128 + 2) * sizeof(float);
 static_assert(MAX_CTAS * sizeof(unsigned int) <= WS_HEAD, "counters");

@@ -307,9 +307,10 @@ int attn_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes
  *   mask_kind, window, keep_first  as in attn_bwd: kept initial keys go with
  *           ATTN_MASK_SLIDING_WINDOW (the streaming mask)
  *   workspace  device memory of attn_decode_kv4_workspace_bytes() bytes, 16-byte
- *           aligned, filled with zeros before its first use; every call leaves it
- *           ready for the next.  Calls that share a workspace must be ordered;
- *           calls with workspaces of their own may overlap, captured or not.
+ *           aligned, its first ATTN_DECODE_KV4_WORKSPACE_ZERO bytes filled with
+ *           zeros before its first use; every call leaves it ready for the next.
+ *           Calls that share a workspace must be ordered; calls with workspaces of
+ *           their own may overlap, captured or not.
  * A key that the masks hide from a row takes no part in it, whatever the cache
  * holds (blocks with a NaN among them).  A row that sees no key gets out = 0 and
  * lse = -inf (lse = s with a sink).  The call must be decode-shaped,
@@ -322,6 +323,8 @@ int attn_decode_kv4(const void* q, const void* k_codes, const void* k_scales, co
                     const void* v_scales, void* out, float* lse, int N, int Hq, int H, int L, int S, int C, int E,
                     int Ev, float scale, int mode, const float* sink_logits, int mask_kind, int window,
                     int keep_first, const int* kv_len, void* workspace, size_t workspace_bytes, void* stream);
+
+#define ATTN_DECODE_KV4_WORKSPACE_ZERO 4096
 
 /* Bytes of workspace that attn_decode_kv4 needs, the same for every call. */
 size_t attn_decode_kv4_workspace_bytes(void);

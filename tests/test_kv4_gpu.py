@@ -272,6 +272,41 @@ def test_decode_ragged_lengths(mask, window, keep, sink, mode):
                seed=window % 97 + keep % 89, length=512)
 
 
+@pytest.mark.parametrize("E,Ev", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("mode", ["dot", "rbf"])
+@pytest.mark.parametrize("group,L", [(4, 1), (9, 1), (4, 4)])
+def test_decode_head_widths(group, L, mode, E, Ev):
+    """Both row counts of the kernel (up to 8, up to 16 query rows) at every pair of head widths, whole and split units."""
+    run_decode(2, 2 * group, 2, L, 1296, E, Ev, [1290, 530], mode=mode, mask="streaming", window=600, keep=130, sink=True, seed=E + Ev + L)
+
+
+def test_decode_lengths_beyond_the_given_length():
+    """kv_len is clamped to [0, length]."""
+    rng = np.random.default_rng(21)
+    cpu, k, v = ku.random_cache(rng, 4, 2, 96, 64, 64)
+    q = ku.bf16(rng.standard_normal((4, 4, 1, 64)))
+    out, lse = attn.attn_decode_kv4(q.cuda(), to_gpu(cpu), scale=0.125, length=70, kv_len=ints([70, 1000, -3, 2**31 - 1]))
+    ref = orc4.attention(ku.f64(q), k, v, [70, 70, 0, 70], scale=0.125)
+    ku.compare(out, lse, *ref, v_most=float(np.abs(v).max()), scale_of_logits=16.0)
+
+
+def test_decode_slices_of_a_cache():
+    """Part of a cache's batch (its rows are contiguous), and no lse."""
+    rng = np.random.default_rng(22)
+    cpu, k, v = ku.random_cache(rng, 5, 2, 80, 128, 64)
+    cache = attn.KV4Cache(*(t[1:4] for t in to_gpu(cpu)))
+    q = ku.bf16(rng.standard_normal((3, 4, 1, 128)))
+    lens = [80, 3, 41]
+    out, lse = attn.attn_decode_kv4(q.cuda(), cache, scale=0.09, kv_len=ints(lens))
+    ref = orc4.attention(ku.f64(q), k[1:4], v[1:4], lens, scale=0.09)
+    ku.compare(out, lse, *ref, v_most=float(np.abs(v).max()), scale_of_logits=16.0)
+    qg, ws, out2, kv_len = q.cuda(), attn.kv4_workspace(), torch.empty_like(out), ints(lens)
+    st = attn.attn_decode_kv4_raw(qg.data_ptr(), *(t.data_ptr() for t in cache), out2.data_ptr(), None, 3, 4, 2, 1, 80, 80, 128, 64,
+                                  0.09, 0, None, 0, 0, 0, kv_len.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                  torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and torch.equal(out, out2)
+
+
 def test_decode_all_sequences_empty():
     run_decode(3, 4, 2, 1, 16, 64, 64, [0, 0, 0], length=16)
     run_decode(3, 4, 2, 1, 16, 128, 128, [0, 0, 0], length=16, sink=True)
@@ -501,6 +536,34 @@ def test_offsets_past_32_bits():
     out, lse = attn.attn_decode_kv4(q.cuda(), cache, scale=0.1, mask_kind="window", window=L - 1)
     ref = orc4.attention(ku.f64(q), kq, vq, [L], scale=0.1, mask_kind="window", window=L - 1)
     ku.compare(out, lse, *ref, v_most=float(np.abs(vq).max()), scale_of_logits=16.0)
+    # and with kept first keys: the chunks between them and the window are not read
+    kf, vf = ku.random_rows(rng, (1, 1, 3, E)), ku.random_rows(rng, (1, 1, 3, E))
+    attn.attn_kv4_write(cache, kf.cuda(), vf.cuda())
+    out, lse = attn.attn_decode_kv4(q.cuda(), cache, scale=0.1, mask_kind="streaming", window=L - 1, keep_first=3)
+    kq, vq = (np.concatenate([orc4.dequantise(*orc4.quantise(ku.f64(x))), y], 2) for x, y in ((kf, kq), (vf, vq)))
+    ref = orc4.attention(ku.f64(q), kq, vq, [L + 3], scale=0.1, mask_kind="streaming", window=L - 1, keep=3)
+    ku.compare(out, lse, *ref, v_most=float(np.abs(vq).max()), scale_of_logits=16.0)
+
+
+def test_a_prompt_piece_attends_through_the_read_rows():
+    """Prompt pieces longer than a decode call: each piece is written, the rows so far come back in bf16 and go through
+    the causal forward."""
+    rng = np.random.default_rng(23)
+    N, Hq, H, E, C = 2, 4, 2, 64, 224
+    cache = attn.kv4_cache(N, H, C, E)
+    k, v = ku.random_rows(rng, (N, H, 200, E)), ku.random_rows(rng, (N, H, 200, E))
+    kq, vq = (orc4.dequantise(*orc4.quantise(ku.f64(x))) for x in (k, v))
+    done = 0
+    for piece in (130, 70):
+        q = ku.bf16(rng.standard_normal((N, Hq, piece, E)))
+        attn.attn_kv4_write(cache, k[:, :, done:done + piece].cuda(), v[:, :, done:done + piece].cuda(), start=done)
+        done += piece
+        kb, vb = attn.attn_kv4_read(cache, done)
+        out, lse = attn.attn_fwd(q.cuda(), kb, vb, scale=0.125, mask_kind="causal")
+        ref, ref_lse = orc4.attention(ku.f64(q), kq, vq, [done] * N, scale=0.125, mask_kind="causal")
+        err = np.linalg.norm(ku.f64(out) - ref) / np.linalg.norm(ref)
+        # two bf16 roundings (P and the output), each at most 2^-8 of its value and on average well under half of that
+        assert err <= 2.0 ** -8 and np.abs(ku.f64(lse) - ref_lse).max() <= 1e-3
 
 
 def test_binding_refusals():
