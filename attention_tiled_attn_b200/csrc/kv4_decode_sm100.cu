@@ -52,6 +52,7 @@ constexpr int NQ = 4;           // units whose query rows may be on chip
 constexpr int MAX_CTAS = 160;   // grid limit, which sizes the workspace
 constexpr int UNIT_COST = 4;    // a unit's beginning and end, in chunks, when the work is split
 constexpr int MIN_SHARE = 4;    // chunks of a CTA's share, at least
+constexpr int FEW = 4;          // partials of a unit that are merged in one round of loads
 constexpr int NO_SPLIT = 6;     // a unit of so many chunks is never split
 constexpr float RESCALE = 8.f;  // the running maximum follows the true one within 2^8
 constexpr float P_SHIFT = 7.f;  // P is held times 2^7
@@ -100,7 +101,8 @@ struct Cfg {
   static constexpr int OFF_Q = OFF_MERGE + NBUF * NCW * NX * 16;  // [NQ][8 NT][E] bf16
   static constexpr int OFF_ML = OFF_Q + NQ * Q_SLOT;              // [NBUF][NCW][8 NT] float2
   static constexpr int OFF_WT = OFF_ML + NBUF * NCW * 8 * NT * 8; // [NCW][8 NT] float: weights of the warps' states
-  static constexpr int OFF_BAR = OFF_WT + NCW * 8 * NT * 4;
+  static constexpr int OFF_OWT = OFF_WT + NCW * 8 * NT * 4;       // [8 NT] float: weights of the next CTA's partial
+  static constexpr int OFF_BAR = OFF_OWT + 8 * NT * 4;
   static constexpr int NBAR = 2 * NSTAGE + 2 * NQ + 2 * NBUF;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;             // Misc
   static constexpr int SMEM = OFF_MISC + 128;
@@ -113,6 +115,7 @@ struct Cfg {
 struct Misc {
   int abort_flag;
   int n_pending;         // split units that this CTA completed
+  int there;             // the other CTAs' partials of the segment at hand are complete
   unsigned pending[2];   // their numbers ...
   unsigned pend_u0[2];   // ... and first positions in the work list
   unsigned pend_nc[2];
@@ -320,6 +323,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
   float4* merge = reinterpret_cast<float4*>(smem + C::OFF_MERGE);
   float2* merge_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
   float* wts = reinterpret_cast<float*>(smem + C::OFF_WT);
+  float* other_wts = reinterpret_cast<float*>(smem + C::OFF_OWT);
   auto full_bar = [&](unsigned s) -> uint32_t { return sb + C::OFF_BAR + 8u * s; };
   auto empty_bar = [&](unsigned s) -> uint32_t { return sb + C::OFF_BAR + 8u * (C::NSTAGE + s); };
   auto qfull_bar = [&](unsigned k) -> uint32_t { return sb + C::OFF_BAR + 8u * (2 * C::NSTAGE + k % NQ); };
@@ -436,6 +440,37 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     const int mt = tid - (NCW + NPROD) * 32;
     bool ok = true;
     for (; more; more = w.next(p)) {
+      const bool whole = w.whole();
+      unsigned b0 = 0, nseg = 1;
+      if (!whole) {
+        b0 = split.cta_of(w.u0 + UNIT_COST);
+        nseg = split.cta_of(w.u0 + UNIT_COST + w.s.nc - 1) - b0 + 1;
+      }
+      // A unit shared with the next CTA alone, which had its part of it first: if that partial is complete before this
+      // one, the unit is finished here and this one never written out.  The counter is watched while the consumers
+      // are still at work.
+      bool there = false;
+      float2 other_ml = make_float2(-INFINITY, 0.f);
+      const float* other = p.partials + static_cast<size_t>(2 * (blockIdx.x + 1)) * (WS_SLOT / 4);
+      if (__builtin_expect(nseg == 2 && w.lo == 0, 0)) {
+        if (mt == 0) {
+          const long long t0 = clock64();
+          bool all = false;
+          while (true) {
+            const bool last = mbar_try_wait(mfull_bar(w.k), (w.k / C::NBUF) & 1);
+            unsigned v;
+            asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p.counters + b0) : "memory");
+            all = v == 1;
+            if (all || last || clock64() - t0 > WAIT_LIMIT_CYCLES) break;
+            __nanosleep(500);
+          }
+          if (all) __threadfence();  // the counter's reading before the partial's
+          misc->there = all;
+        }
+        merge_bar();
+        there = misc->there != 0;
+        if (there && mt % (8 * NT) < p.R) other_ml = __ldcg(reinterpret_cast<const float2*>(other + MAX_ROWS * 128) + mt % (8 * NT));
+      }
       ok = mbar_sleep(mfull_bar(w.k), (w.k / C::NBUF) & 1);
       // both warps decide together
       uint32_t both;
@@ -453,7 +488,6 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
       const int na = static_cast<int>(min(w.hi - w.lo, static_cast<unsigned>(NG))) * GW;
       const int w0 = static_cast<int>(w.i0 % NG) * GW;
       auto nth = [&](int y) { return w0 + y < NCW ? w0 + y : w0 + y - NCW; };
-      const bool whole = w.whole();
       float* mine = p.partials + static_cast<size_t>(2 * blockIdx.x + (w.lo == 0 ? 1 : 0)) * (WS_SLOT / 4);
       const float4* buf = merge + (w.k % C::NBUF) * NCW * NX;
       const float2* buf_ml = merge_ml + (w.k % C::NBUF) * NCW * 8 * NT;
@@ -470,12 +504,22 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
         }
 #pragma unroll
         for (int y = 0; y < NCW; ++y) l = fmaf(e[y].y, e[y].x == -INFINITY ? 0.f : ex2(e[y].x - M), l);
+        if (__builtin_expect(there, 0)) {  // r is the row of other_ml too: the stride of z is a multiple of 8 NT
+          const float own = M;
+          M = fmaxf(M, other_ml.x);
+          l = l * (own == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(own - M)) +
+              other_ml.y * (other_ml.x == -INFINITY ? (other_ml.y == 0.f ? 0.f : 1.f) : ex2(other_ml.x - M));
+        }
         const float m = buf_ml[me * 8 * NT + r].x;
         float wt = m == -INFINITY ? 0.f : ex2(m - M);
-        if (whole) {
+        if (whole || there) {
           float lse;
-          wt *= row_factor(M, l, p.sink ? __ldg(p.sink + w.h * p.group + r / p.L) * LOG2E : -INFINITY, &lse);
-          if (me == w0 && p.lse) p.lse[w.unit(p) * p.R + r] = lse;
+          const float f = row_factor(M, l, p.sink ? __ldg(p.sink + w.h * p.group + r / p.L) * LOG2E : -INFINITY, &lse);
+          wt *= f;
+          if (me == w0) {
+            if (p.lse) p.lse[w.unit(p) * p.R + r] = lse;
+            if (there) other_wts[r] = other_ml.x == -INFINITY ? 0.f : ex2(other_ml.x - M) * f;
+          }
         } else if (me == w0) {
           reinterpret_cast<float2*>(mine + MAX_ROWS * 128)[r] = make_float2(M, l);
         }
@@ -490,6 +534,14 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
         float4 acc[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (__builtin_expect(there, 0)) {
+          const float f0 = other_wts[r], f1 = r + 1 < p.R ? other_wts[r + 1] : 0.f;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(other) + t * MD * 32 + i * NMERGE * 32 + mt);
+            acc[i] = make_float4(v.x * f0, v.y * f1, v.z * f0, v.w * f1);
+          }
+        }
         for (int y0 = 0; y0 < na; y0 += GW) {
 #pragma unroll
           for (int y = 0; y < GW; ++y) {
@@ -508,19 +560,20 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
           const int x = t * MD * 32 + i * NMERGE * 32 + mt;
-          if (whole)
+          if (whole || there)
             store_out<EV, MD>(p, w.unit(p), x, acc[i]);
           else
             reinterpret_cast<float4*>(mine)[x] = acc[i];
         }
       }
-      if (!whole) __threadfence();
+      if (!whole && !there) __threadfence();
       merge_bar();
       if (mt == 0) {
         mbar_arrive(mempty_bar(w.k));
-        if (!whole) {
-          const unsigned b0 = split.cta_of(w.u0 + UNIT_COST), b1 = split.cta_of(w.u0 + UNIT_COST + w.s.nc - 1);
-          if (atomicInc(p.counters + b0, b1 - b0) == b1 - b0) {
+        if (there) {
+          p.counters[b0] = 0u;  // the other has counted
+        } else if (!whole) {
+          if (atomicInc(p.counters + b0, nseg - 1) == nseg - 1) {
             const int x = misc->n_pending++;
             misc->pending[x] = static_cast<unsigned>(w.unit(p));
             misc->pend_u0[x] = w.u0;
@@ -904,7 +957,6 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
     const int nseg = static_cast<int>(split.cta_of(misc->pend_u0[x0] + UNIT_COST + misc->pend_nc[x0] - 1) - b0) + 1;
     auto slot = [&](int y) { return p.partials + static_cast<size_t>(2 * (b0 + y) + (y == 0 ? 1 : 0)) * (WS_SLOT / 4); };
     const int h = static_cast<int>(unit % p.H);
-    constexpr int FEW = 4;
     if (nseg <= FEW) {  // each thread finds its two rows' weights itself: one round of loads
       for (int x = tid; x < NX; x += C::THREADS) {
         const int r = 8 * (x / (32 * MD)) + 2 * (x & 3);
