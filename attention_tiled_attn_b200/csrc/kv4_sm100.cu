@@ -56,9 +56,10 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 }
 
 // Blocks of 16 per thread.  64 bytes of values in flight per thread and small CTAs measured best: bf16 2 blocks (4 x
-// 8192 x 8 rows of 128 + 128 written in 32 us; 1 block 37, 4 blocks of 256 threads 40; 131072 x 8 rows read in 105 us,
-// 6.5 TB/s; 1 block 113), fp32 1 block (written in 45 us; 2 blocks 49).  bf16 calls whose tiles of 2 would leave SMs
-// without a CTA take 1.
+// 8192 x 8 rows of 128 + 128 written in 32 us; 1 block 37, 4 blocks of 256 threads 40; 131072 x 8 rows read in 103 us,
+// 6.7 TB/s; 1 block 113), fp32 1 block (written in 45 us; 2 blocks 49).  bf16 calls whose tiles of 2 would leave SMs
+// without a CTA take 1.  Writing, the two are WT blocks apart: its loads miss every cache, and a warp's 32-byte pieces
+// then make whole lines (strided sources 32 us against 34).  Reading, they are neighbours, which share their address.
 template <bool BF16>
 constexpr int WIDE = BF16 ? 2 : 1;
 
@@ -126,54 +127,59 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   return d;
 }
 
-template <bool BF16, int BPT>
+template <bool BF16, int PER>
 __global__ void __launch_bounds__(WT) kv4_write_kernel(const Kv4WriteArgs a) {
   overlap_start();
-  const Place<WT * BPT> at(a.E, a.Ev, a.N, a.H, a.L);
+  const Place<WT * PER> at(a.E, a.Ev, a.N, a.H, a.L);
   constexpr int SIZE = BF16 ? 2 : 4, WORDS = BF16 ? 1 : 2;  // bytes of a value, 32-byte pieces of a block
   const char* src = static_cast<const char*>(at.v ? a.v : a.k);
   const size_t sn = (at.v ? a.v_sn : a.k_sn) * SIZE, sh = (at.v ? a.v_sh : a.k_sh) * SIZE, sl = (at.v ? a.v_sl : a.k_sl) * SIZE;
   const bool wide = ((reinterpret_cast<uintptr_t>(src) | sn | sh | sl) & 31) == 0;
-  uint2* codes_out = static_cast<uint2*>(at.v ? a.v_codes : a.k_codes);
-  uint8_t* scales_out = static_cast<uint8_t*>(at.v ? a.v_scales : a.k_scales);
+  // the thread's blocks are WT apart (neighbouring threads load neighbouring bytes), which is dr rows of one column
+  const unsigned dr = WT >> at.shift;
+  const int column = at.block(threadIdx.x);
   overlap_wait();
-  // for the tile's first (n, h)
-  const char* src0 = src + at.n0 * sn + (at.nh0 - at.n0 * a.H) * sh;
-  const long long to0 = static_cast<long long>(at.nh0) * a.C;
-  const int pos0 = a.pos ? __ldg(a.pos + at.n0) : a.start, count0 = a.count ? __ldg(a.count + at.n0) : a.L;
-
-  uint32_t in[BPT][WORDS][8];
-  long long to[BPT];  // the block's place in the cache, or -1
+  uint32_t in[PER][WORDS][8];
+  long long to[PER];  // the block's place in the cache, or -1
+  const char* p = src;
+  long long unit = 0;
+  unsigned l = 0;
+  int pos = 0, count = 0;
 #pragma unroll
-  for (int i = 0; i < BPT; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int x = i * WT + threadIdx.x;
-    unsigned l = at.row(x);
-    const char* p = src0;
-    long long unit = to0;
-    int pos = pos0, count = count0;
     to[i] = -1;
     if (at.first + x >= at.total) continue;
-    if (l >= static_cast<unsigned>(a.L)) {  // past the end of the tile's first (n, h)
-      const unsigned q = l / a.L, nh = at.nh0 + q, n = nh / a.H;
-      l -= q * a.L;
-      p = src + n * sn + (nh - n * a.H) * sh;
+    l += dr;
+    p += dr * sl;
+    if (i == 0 || l >= static_cast<unsigned>(a.L)) {  // the first, or past the end of its (n, h)
+      l = at.row(x);
+      unsigned nh = at.nh0, n = at.n0;
+      if (l >= static_cast<unsigned>(a.L)) {
+        const unsigned q = l / a.L;
+        l -= q * a.L;
+        nh += q;
+        n = nh / a.H;
+      }
+      p = src + n * sn + (nh - n * a.H) * sh + l * sl + column * (KV4_BLOCK * SIZE);
       unit = static_cast<long long>(nh) * a.C;
-      if (a.pos) pos = __ldg(a.pos + n);
-      if (a.count) count = __ldg(a.count + n);
+      pos = a.pos ? __ldg(a.pos + n) : a.start;
+      count = a.count ? __ldg(a.count + n) : a.L;
     }
     const long long row = static_cast<long long>(pos) + l;
     if (row < 0 || row >= a.C || static_cast<int>(l) >= count) continue;
-    to[i] = ((unit + row) << at.shift) + at.block(x);
-    p += l * sl + at.block(x) * (KV4_BLOCK * SIZE);
+    to[i] = ((unit + row) << at.shift) + column;
 #pragma unroll
     for (int y = 0; y < WORDS; ++y) load32(p + 32 * y, wide, in[i][y]);
   }
+  uint2* codes_out = static_cast<uint2*>(at.v ? a.v_codes : a.k_codes);
+  uint8_t* scales_out = static_cast<uint8_t*>(at.v ? a.v_scales : a.k_scales);
 #pragma unroll
-  for (int i = 0; i < BPT; ++i) {
+  for (int i = 0; i < PER; ++i) {
     if (to[i] < 0) continue;
     float x[16], y6;
     if constexpr (BF16) {
-      uint32_t (&w)[8] = in[i][0];
+      const uint32_t (&w)[8] = in[i][0];
       const uint32_t m4 = max_abs2(max_abs2(max_abs2(w[0], w[1]), max_abs2(w[2], w[3])), max_abs2(max_abs2(w[4], w[5]), max_abs2(w[6], w[7])));
       const float most = max_nan(__uint_as_float((m4 & 0x7FFFu) << 16), __uint_as_float(m4 & 0x7FFF0000u));
       y6 = __uint_as_float((__float_as_uint(most * (1.f / 6.f)) + 0x80u) & 0xFFFFFF00u);
@@ -224,63 +230,61 @@ __device__ __forceinline__ uint32_t half2_to_bf162(uint32_t h) {  // exact for t
   return pack_bf16x2(f.x, f.y);
 }
 
-template <bool BF16, int BPT>
+template <bool BF16, int PER>
 __global__ void __launch_bounds__(WT) kv4_read_kernel(const Kv4ReadArgs a) {
   overlap_start();
-  const Place<WT * BPT> at(a.E, a.Ev, a.N, a.H, a.rows);
-  char* dst = static_cast<char*>(at.v ? a.v : a.k);
-  const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
-  const uint2* codes_in = static_cast<const uint2*>(at.v ? a.v_codes : a.k_codes);
-  const uint8_t* scales_in = static_cast<const uint8_t*>(at.v ? a.v_scales : a.k_scales);
+  const Place<WT * PER> at(a.E, a.Ev, a.N, a.H, a.rows);
+  constexpr int SIZE = BF16 ? 2 : 4;
+  const int first = threadIdx.x * PER;  // of the thread's blocks, which are of one row
+  if (at.first + first >= at.total) {
+    overlap_wait();
+    return;
+  }
+  unsigned r = at.row(first), nh = at.nh0, n = at.n0;
+  if (r >= static_cast<unsigned>(a.rows)) {  // past the end of the tile's first (n, h)
+    const unsigned q = r / a.rows;
+    r -= q * a.rows;
+    nh += q;
+    n = nh / a.H;
+  }
   overlap_wait();
-  // for the tile's first (n, h)
-  const long long from0 = static_cast<long long>(at.nh0) * a.C;
-  const int pos0 = a.pos ? __ldg(a.pos + at.n0) : a.start, end0 = a.kv_len ? min(__ldg(a.kv_len + at.n0), a.C) : a.C;
-  uint2 codes[BPT];
-  uint32_t scale[BPT];
-  bool live[BPT];
+  const long long row = static_cast<long long>(a.pos ? __ldg(a.pos + n) : a.start) + r;
+  uint2 codes[PER];
+  uint32_t bytes = 0;
 #pragma unroll
-  for (int i = 0; i < BPT; ++i) {
-    const int x = i * WT + threadIdx.x;
-    unsigned r = at.row(x);
-    long long unit = from0;
-    int pos = pos0, end = end0;
-    live[i] = at.first + x < at.total;
-    codes[i] = make_uint2(0u, 0u);
-    scale[i] = 0u;
-    if (!live[i]) continue;
-    if (r >= static_cast<unsigned>(a.rows)) {  // past the end of the tile's first (n, h)
-      const unsigned q = r / a.rows, nh = at.nh0 + q;
-      r -= q * a.rows;
-      unit = static_cast<long long>(nh) * a.C;
-      if (a.pos) pos = __ldg(a.pos + nh / a.H);
-      if (a.kv_len) end = min(__ldg(a.kv_len + nh / a.H), a.C);
-    }
-    const long long row = static_cast<long long>(pos) + r;
-    if (row >= 0 && row < end) {
-      const long long from = ((unit + row) << at.shift) + at.block(x);
-      codes[i] = __ldg(codes_in + from);
-      scale[i] = __ldg(scales_in + from);
+  for (int i = 0; i < PER; ++i) codes[i] = make_uint2(0u, 0u);
+  if (row >= 0 && row < (a.kv_len ? min(__ldg(a.kv_len + n), a.C) : a.C)) {
+    const size_t from = ((static_cast<size_t>(nh) * a.C + row) << at.shift) + at.block(first);
+    const uint2* codes_in = static_cast<const uint2*>(at.v ? a.v_codes : a.k_codes) + from;
+    const uint8_t* scales_in = static_cast<const uint8_t*>(at.v ? a.v_scales : a.k_scales) + from;
+    if constexpr (PER == 2) {
+      const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes_in));
+      codes[0] = make_uint2(c.x, c.y);
+      codes[1] = make_uint2(c.z, c.w);
+      bytes = __ldg(reinterpret_cast<const uint16_t*>(scales_in));
+    } else {
+      codes[0] = __ldg(codes_in);
+      bytes = __ldg(scales_in);
     }
   }
+  char* dst = static_cast<char*>(at.v ? a.v : a.k);
+  const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+  dst += (at.first + first) * (KV4_BLOCK * SIZE);
 #pragma unroll
-  for (int i = 0; i < BPT; ++i) {
-    if (!live[i]) continue;
-    const uint32_t s2 = kv4_scale2(scale[i]);
-    uint32_t h[8];
-    uint32_t c[4];
+  for (int i = 0; i < PER; ++i) {
+    const uint32_t s2 = kv4_scale2((bytes >> (8 * i)) & 0xFFu);
+    uint32_t h[8], c[4];
     kv4_unpack8(codes[i].x, c);
 #pragma unroll
     for (int y = 0; y < 4; ++y) h[y] = hmul2(c[y], s2);
     kv4_unpack8(codes[i].y, c);
 #pragma unroll
     for (int y = 0; y < 4; ++y) h[4 + y] = hmul2(c[y], s2);
-    char* p = dst + (at.first + i * WT + threadIdx.x) * KV4_BLOCK * (BF16 ? 2 : 4);
     uint32_t w[8];
     if constexpr (BF16) {
 #pragma unroll
       for (int y = 0; y < 8; ++y) w[y] = half2_to_bf162(h[y]);
-      store32(p, wide, w);
+      store32(dst + 32 * i, wide, w);
     } else {
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
@@ -290,14 +294,14 @@ __global__ void __launch_bounds__(WT) kv4_read_kernel(const Kv4ReadArgs a) {
           w[2 * y] = __float_as_uint(f.x);
           w[2 * y + 1] = __float_as_uint(f.y);
         }
-        store32(p + 32 * z, wide, w);
+        store32(dst + 64 * i + 32 * z, wide, w);
       }
     }
   }
 }
 
-unsigned tiles(int N, int H, int rows, int E, int Ev, int bpt) {
-  const long long all = static_cast<long long>(N) * H * rows, tile = WT * bpt;
+unsigned tiles(int N, int H, int rows, int E, int Ev, int per) {
+  const long long all = static_cast<long long>(N) * H * rows, tile = WT * per;
   return static_cast<unsigned>((all * (E / KV4_BLOCK) + tile - 1) / tile + (all * (Ev / KV4_BLOCK) + tile - 1) / tile);
 }
 // whether tiles of 2 blocks per thread give every SM a few CTAs
@@ -305,13 +309,13 @@ bool many(int N, int H, int rows, int E, int Ev, int num_sms) {
   return tiles(N, H, rows, E, Ev, 2) >= 4u * static_cast<unsigned>(num_sms);
 }
 
-template <bool BF16, int BPT>
+template <bool BF16, int PER>
 cudaError_t write_rows(const Kv4WriteArgs& a, cudaStream_t stream) {
-  return launch_overlapped(kv4_write_kernel<BF16, BPT>, tiles(a.N, a.H, a.L, a.E, a.Ev, BPT), WT, 0, stream, a);
+  return launch_overlapped(kv4_write_kernel<BF16, PER>, tiles(a.N, a.H, a.L, a.E, a.Ev, PER), WT, 0, stream, a);
 }
-template <bool BF16, int BPT>
+template <bool BF16, int PER>
 cudaError_t read_rows(const Kv4ReadArgs& a, cudaStream_t stream) {
-  return launch_overlapped(kv4_read_kernel<BF16, BPT>, tiles(a.N, a.H, a.rows, a.E, a.Ev, BPT), WT, 0, stream, a);
+  return launch_overlapped(kv4_read_kernel<BF16, PER>, tiles(a.N, a.H, a.rows, a.E, a.Ev, PER), WT, 0, stream, a);
 }
 
 }  // namespace
