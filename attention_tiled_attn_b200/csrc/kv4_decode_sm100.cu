@@ -1,15 +1,23 @@
 // Decode attention over the 4-bit cache (format: kv4.cuh), split over keys.
 //
-// The pass is bound by the cache's bytes: 9/16 of a byte per value, each read once.  As in the
-// bf16 decode, the visible keys of every (batch, KV head) unit are cut into 64-key chunks and
-// the list of all chunks is split evenly over a persistent grid, one CTA per SM; a CTA may end
-// one unit and begin the next.  With per-sequence lengths the list is known on the device only,
-// so each CTA sums the lengths and finds its own share.
+// The pass reads 9/16 of a byte per cached value once, so HBM bounds long caches; per value it
+// costs a conversion, a scaling and a tensor-core operand slot, which come close behind (a work
+// copy without the loads takes as long as one without the arithmetic).  As in the bf16 decode, the
+// visible keys of every (batch, KV head) unit are cut into chunks (128 keys) and the list of all
+// chunks is split evenly over a persistent grid, one CTA per SM; a CTA may end one unit and begin
+// the next.  With per-sequence lengths the list is known on the device only, so each CTA sums the
+// lengths and finds its own share.
 //
-// Per CTA: one producer thread copies whole chunks (elements and scales are contiguous per unit,
-// so a chunk is four bulk copies) through a ring of stages; consumer warp w takes every 8th
-// chunk alone.  The keys form the M side of m16n8k16 products, so that 8 query rows cost one
-// instruction and not two half-empty ones:
+// Per CTA, connected by mbarriers:
+//   producer warps   one thread each copies whole chunks (elements and scales are contiguous per
+//                    unit: four bulk copies) into a ring of stages, and each unit's query rows;
+//   consumer groups  take the chunks in turn, the warps of a group sharing a chunk by keys; a group
+//                    goes on to the next unit without waiting for the others;
+//   merging warps    join the states of a unit's warps once all have left it, and finish the unit
+//                    or write the CTA's part of it.
+//
+// The keys form the M side of m16n8k16 products, so that 8 query rows cost one instruction and not
+// two half-empty ones:
 //   S^T (16 keys x 8 rows)  = K Q^T      A = 16 keys, from registers
 //   O^T (16 dims x 8 rows) += V^T P^T    A = 16 value dimensions x 16 keys, from registers
 // A thread's A fragment of K is 4 dimensions of a key per product.  Any order of the reduction's
@@ -17,16 +25,22 @@
 // its key: one 16-byte (E = 128) shared load.  Elements become fp16 by the conversion
 // instruction and are multiplied by their scale, exactly.  V's fragment pairs two keys of one
 // dimension: the elements of the two keys are interleaved as bytes before the conversion.
-// P^T's fragment is S^T's transposed 8 x 8 blocks (movmatrix).
+// P^T's fragment is S^T's transposed 8 x 8 blocks (movmatrix).  tcgen05's 128-row tiles would be
+// mostly padding here, and its block-scaled kinds take neither these scales nor an fp16 Q.
 //
 // Q is held in fp16 with each row shifted by a power of two, so that its largest element is in
-// [2^14, 2^15): nothing above 2^-31 of it is lost.  P is rounded to fp16 with 2^7 of headroom used
-// below the running maximum (p <= 2^8 before the shift, see RESCALE), so that probabilities down to
-// 2^-21 of the row's largest keep 11 bits; sums, maxima and outputs are fp32.
+// [2^14, 2^15): nothing above 2^-31 of it is lost.  P is rounded to fp16 times 2^7 (p is at most
+// 2^8 before that, see RESCALE): 11 bits down to 2^-21 of the running maximum's probability, an
+// absolute 2^-32 below.  Sums, maxima and outputs are fp32.
 //
 // A unit inside one CTA is finished there.  Otherwise each CTA writes its (m, l, O) and counts it;
-// the CTA whose count completes the unit merges them.  The counter wraps to zero with the last
-// count (atomicInc), so no launch has to clear it.
+// the CTA whose count completes the unit merges them at its end.  A unit shared with the next CTA
+// alone is finished by the first of the two, whose part comes last, without writing that.  The
+// counter wraps to zero with the last count (atomicInc), so no launch has to clear it.
+//
+// Measured (one B200, device time): 16 x 131072 x 8 heads of 128 + 128 in 390 to 430 us (2.42 GB,
+// 5.6 to 6.2 TB/s of 6.47 measured copy; 473 us back to back, under the power cap); 32 sequences of
+// up to 4096 rows, 8 heads, 27 us; one of 130 rows 6 us.
 
 #include <atomic>
 #include <cstdint>
@@ -50,10 +64,14 @@ constexpr int NPROD = 2;        // producer warps (one thread each)
 constexpr int NMERGE = 2;       // merging warps
 constexpr int NQ = 4;           // units whose query rows may be on chip
 constexpr int MAX_CTAS = 160;   // grid limit, which sizes the workspace
-constexpr int UNIT_COST = 4;    // a unit's beginning and end, in chunks, when the work is split
-constexpr int MIN_SHARE = 4;    // chunks of a CTA's share, at least
+// What a unit costs besides its chunks, in chunks, when the work is split: 32 ragged sequences of up to 4096 rows take
+// 28 us with 4, 32 with 2, 37 with 1; 5 and 6 change nothing more.
+constexpr int UNIT_COST = 4;
+// A CTA's share, at least (chunks and unit costs): one sequence of 2000 rows takes 12.2 us with 4, 13.0 with 6, 18 with
+// 12; 3 changes nothing more.
+constexpr int MIN_SHARE = 4;
 constexpr int FEW = 4;          // partials of a unit that are merged in one round of loads
-constexpr int NO_SPLIT = 6;     // a unit of so many chunks is never split
+constexpr int NO_SPLIT = 6;     // a unit of so many chunks is never split (3 and 12 measure the same)
 constexpr float RESCALE = 8.f;  // the running maximum follows the true one within 2^8
 constexpr float P_SHIFT = 7.f;  // P is held times 2^7
 constexpr size_t WS_HEAD = ATTN_DECODE_KV4_WORKSPACE_ZERO;  // arrival counters, one per CTA
@@ -106,7 +124,7 @@ struct Cfg {
   static constexpr int NBAR = 2 * NSTAGE + 2 * NQ + 2 * NBUF;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;             // Misc
   static constexpr int SMEM = OFF_MISC + 128;
-  // the merge of a unit's partials keeps its sums, then its weights, where the warps' fragments and the stages were
+  // the merge of a unit's partials keeps its weights where the stages were and its sums where the warps' fragments were
   static constexpr int PARTS = 2 * THREADS / NX > 1 ? 2 * THREADS / NX : 1;
   static_assert(MAX_CTAS * 8 * NT * 4 <= NSTAGE * STAGE && PARTS <= NCW, "combine buffers");
   static_assert(SMEM <= 232448, "shared memory budget");
@@ -115,7 +133,7 @@ struct Cfg {
 struct Misc {
   int abort_flag;
   int n_pending;         // split units that this CTA completed
-  int there;             // the other CTAs' partials of the segment at hand are complete
+  int there;             // the next CTA's partial of the unit at hand is complete
   unsigned pending[2];   // their numbers ...
   unsigned pend_u0[2];   // ... and first positions in the work list
   unsigned pend_nc[2];

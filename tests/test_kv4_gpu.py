@@ -155,6 +155,44 @@ def test_strided_and_repeated_sources(dtype):
     check_stored(a.v_codes[:, :, :L], a.v_scales[:, :, :L], v1)
 
 
+@pytest.mark.parametrize("E,Ev,dtype", [(128, 128, torch.bfloat16), (64, 128, torch.bfloat16), (128, 64, torch.float32)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_many_ragged_rows(E, Ev, dtype, shift):
+    """Enough rows for the kernels' wider forms: tiles that end inside a unit, sequences cut by count and by the cache's
+    end, sources and outputs aligned to 16 bytes only (shift), and every other byte of the cache as it was."""
+    rng = np.random.default_rng(E + shift)
+    N, H, L, C = 7, 3, 901, 912
+    per16 = 128 // torch.finfo(dtype).bits  # values in 16 bytes
+    k, v = (ku.random_rows(rng, (N, H, L, w), dtype).cuda() for w in (E, Ev))
+    if shift:
+        def shifted(t):
+            flat = torch.empty(t.numel() + per16, dtype=t.dtype, device="cuda")
+            flat[per16:] = t.reshape(-1)
+            return flat[per16:].view(t.shape)
+        k, v = shifted(k), shifted(v)
+    pos, count = [0, 3, 11, 100, -7, 0, 905], [901, 900, 901, 901, 901, 450, 901]
+    cache = filled(N, H, C, E, Ev)
+    before = [t.clone() for t in cache]
+    attn.attn_kv4_write(cache, k, v, pos=ints(pos), count=ints(count))
+    lens = [max(0, min(C, p + c)) for p, c in zip(pos, count)]
+    kout, vout = (torch.full((N * H * 905 * w + per16,), 7.0, dtype=dtype, device="cuda")[shift * per16:][:N * H * 905 * w].view(N, H, 905, w)
+                  for w in (E, Ev))
+    attn.attn_kv4_read(cache, 905, start=5, kv_len=ints(lens), dtype=dtype, k_out=kout, v_out=vout)
+    for src, got, codes, scales, old_c, old_s in ((k, kout, *cache[:2], *before[:2]), (v, vout, *cache[2:], *before[2:])):
+        for n in range(N):
+            a, b = max(0, pos[n]), lens[n]  # cache rows written
+            check_stored(codes[n, :, a:b], scales[n, :, a:b], src[n, :, a - pos[n]:b - pos[n]])
+            for t, old in ((codes, old_c), (scales, old_s)):
+                assert torch.equal(t[n, :, :a], old[n, :, :a]) and torch.equal(t[n, :, b:], old[n, :, b:])
+            want = np.zeros((H, 905, got.shape[-1]))
+            end = min(910, b)
+            if end > 5:
+                want[:, :end - 5] = stored_values(codes[n, :, 5:end], scales[n, :, 5:end])
+            # what filled() left before the first written row may have scales that no write leaves (infinite values)
+            first = max(0, a - 5)
+            np.testing.assert_array_equal(ku.f64(got[n, :, first:]), want[:, first:])
+
+
 # ------------------------------------------------------------------ reading
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -456,6 +494,42 @@ def test_calls_on_two_streams_overlap():
         for out, lse in got[i][:2] + got[i][-2:]:
             check_call(out, lse, calls[i][2], 0.09)
         assert all(torch.equal(o, got[i][0][0]) for o, _ in got[i])
+
+
+def test_a_whole_step_on_a_stream_that_is_not_current():
+    rng = np.random.default_rng(31)
+    cpu, kh, vh = ku.random_cache(rng, 2, 2, 208, 64, 64)
+    cache = to_gpu(cpu)
+    q = ku.bf16(rng.standard_normal((2, 4, 1, 64)))
+    k1, v1 = ku.random_rows(rng, (2, 2, 1, 64)), ku.random_rows(rng, (2, 2, 1, 64))
+    args = q.cuda(), k1.cuda(), v1.cuda(), ints([200, 17])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    attn.attn_kv4_write(cache, args[1], args[2], pos=ints([199, 16]), stream=side)
+    out, lse = attn.attn_decode_kv4(args[0], cache, scale=0.125, length=200, kv_len=args[3], stream=side)
+    kb, vb = attn.attn_kv4_read(cache, 200, kv_len=args[3], stream=side)
+    side.synchronize()
+    for n, p in enumerate((199, 16)):
+        kh[n, :, p], vh[n, :, p] = (orc4.dequantise(*orc4.quantise(ku.f64(x[n, :, 0]))) for x in (k1, v1))
+    ref = orc4.attention(ku.f64(q), kh, vh, [200, 17], scale=0.125)
+    ku.compare(out, lse, *ref, v_most=float(np.abs(vh).max()), scale_of_logits=16.0)
+    np.testing.assert_array_equal(ku.f64(kb[1, :, :17]), kh[1, :, :17])
+    assert not vb[1, :, 17:].any()
+
+
+def test_a_query_row_that_is_not_finite():
+    """Only its own row is lost."""
+    rng = np.random.default_rng(32)
+    cpu, k, v = ku.random_cache(rng, 1, 1, 304, 128, 128)
+    q = ku.bf16(rng.standard_normal((1, 6, 1, 128)))
+    bad = q.clone()
+    bad[0, 1, 0, 5] = float("nan")
+    bad[0, 4, 0, 7] = float("inf")
+    out, lse = attn.attn_decode_kv4(bad.cuda(), to_gpu(cpu), scale=0.09, length=300)
+    ref, ref_lse = orc4.attention(ku.f64(q), k, v, [300], scale=0.09)
+    ok = [0, 2, 3, 5]
+    ku.compare(out[:, ok], lse[:, ok], ref[:, ok], ref_lse[:, ok], v_most=float(np.abs(v).max()), scale_of_logits=16.0)
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(out[0, 4]).all()
 
 
 def test_captured_step_replays_on_new_inputs():
