@@ -53,7 +53,9 @@ __device__ __forceinline__ uint32_t kv4_scale2(uint32_t byte) { return byte * 0x
 
 // Programmatic dependent launch.  The launches below let a kernel start while the one before it in the stream is still
 // running (the next kernel's start, set-up and scheduling then overlap it); no memory of the caller's is touched
-// before overlap_wait(), which returns once all earlier work of the stream is complete and visible.
+// before overlap_wait(), which returns once all earlier work of the stream is complete and visible.  The kernels read
+// what earlier work may have written with plain loads only: a read-only load (__ldg) may be moved above the wait, and
+// its data must not change while the kernel runs, of which the time before the wait is a part.
 __device__ __forceinline__ void overlap_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void overlap_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

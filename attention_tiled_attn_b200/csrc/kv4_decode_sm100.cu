@@ -152,7 +152,7 @@ struct Seq {
 
 __device__ __forceinline__ Seq sequence(const Params& p, int n) {
   Seq s;
-  s.len = p.kv_len ? min(max(__ldg(p.kv_len + n), 0), p.S) : p.S;
+  s.len = p.kv_len ? min(max(p.kv_len[n], 0), p.S) : p.S;
   const int lo = p.mask_kind >= MASK_WINDOW ? max(0, s.len - p.L - p.window + 1) : 0;
   const int kb_hi = s.len > 0 ? (s.len - 1) / KC + 1 : 1;
   s.nc_head = 0;
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
         float wt = m == -INFINITY ? 0.f : ex2(m - M);
         if (whole || there) {
           float lse;
-          const float f = row_factor(M, l, p.sink ? __ldg(p.sink + w.h * p.group + r / p.L) * LOG2E : -INFINITY, &lse);
+          const float f = row_factor(M, l, p.sink ? p.sink[w.h * p.group + r / p.L] * LOG2E : -INFINITY, &lse);
           wt *= f;
           if (me == w0) {
             if (p.lse) p.lse[w.unit(p) * p.R + r] = lse;
@@ -1003,8 +1003,8 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
           acc = make_float4(fmaf(v[y].x, f0, acc.x), fmaf(v[y].y, f1, acc.y), fmaf(v[y].z, f0, acc.z), fmaf(v[y].w, f1, acc.w));
         }
         float lse0, lse1;
-        const float f0 = row_factor(M0, l0, p.sink ? __ldg(p.sink + h * p.group + r / p.L) * LOG2E : -INFINITY, &lse0);
-        const float f1 = r + 1 < p.R ? row_factor(M1, l1, p.sink ? __ldg(p.sink + h * p.group + (r + 1) / p.L) * LOG2E : -INFINITY, &lse1) : 0.f;
+        const float f0 = row_factor(M0, l0, p.sink ? p.sink[h * p.group + r / p.L] * LOG2E : -INFINITY, &lse0);
+        const float f1 = r + 1 < p.R ? row_factor(M1, l1, p.sink ? p.sink[h * p.group + (r + 1) / p.L] * LOG2E : -INFINITY, &lse1) : 0.f;
         store_out<EV, MD>(p, unit, x, make_float4(acc.x * f0, acc.y * f1, acc.z * f0, acc.w * f1));
         if ((x & 28) == 0 && (x >> 5) % MD == 0 && p.lse) {
           p.lse[static_cast<size_t>(unit) * p.R + r] = lse0;
@@ -1033,7 +1033,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
       float lse;
-      const float f = row_factor(M, l, p.sink ? __ldg(p.sink + h * p.group + r / p.L) * LOG2E : -INFINITY, &lse);
+      const float f = row_factor(M, l, p.sink ? p.sink[h * p.group + r / p.L] * LOG2E : -INFINITY, &lse);
 #pragma unroll
       for (int i = 0; i < (MAX_CTAS + 31) / 32; ++i)
         if (32 * i + lane < nseg) seg_wts[(32 * i + lane) * 8 * NT + r] = e[i].x * f;

@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(WT) kv4_write_kernel(const Kv4WriteArgs a) {
       }
       p = src + n * sn + (nh - n * a.H) * sh + l * sl + column * (KV4_BLOCK * SIZE);
       unit = static_cast<long long>(nh) * a.C;
-      pos = a.pos ? __ldg(a.pos + n) : a.start;
-      count = a.count ? __ldg(a.count + n) : a.L;
+      pos = a.pos ? a.pos[n] : a.start;
+      count = a.count ? a.count[n] : a.L;
     }
     const long long row = static_cast<long long>(pos) + l;
     if (row < 0 || row >= a.C || static_cast<int>(l) >= count) continue;
@@ -248,23 +248,23 @@ __global__ void __launch_bounds__(WT) kv4_read_kernel(const Kv4ReadArgs a) {
     n = nh / a.H;
   }
   overlap_wait();
-  const long long row = static_cast<long long>(a.pos ? __ldg(a.pos + n) : a.start) + r;
+  const long long row = static_cast<long long>(a.pos ? a.pos[n] : a.start) + r;
   uint2 codes[PER];
   uint32_t bytes = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) codes[i] = make_uint2(0u, 0u);
-  if (row >= 0 && row < (a.kv_len ? min(__ldg(a.kv_len + n), a.C) : a.C)) {
+  if (row >= 0 && row < (a.kv_len ? min(a.kv_len[n], a.C) : a.C)) {
     const size_t from = ((static_cast<size_t>(nh) * a.C + row) << at.shift) + at.block(first);
     const uint2* codes_in = static_cast<const uint2*>(at.v ? a.v_codes : a.k_codes) + from;
     const uint8_t* scales_in = static_cast<const uint8_t*>(at.v ? a.v_scales : a.k_scales) + from;
     if constexpr (PER == 2) {
-      const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes_in));
+      const uint4 c = *reinterpret_cast<const uint4*>(codes_in);
       codes[0] = make_uint2(c.x, c.y);
       codes[1] = make_uint2(c.z, c.w);
-      bytes = __ldg(reinterpret_cast<const uint16_t*>(scales_in));
+      bytes = *reinterpret_cast<const uint16_t*>(scales_in);
     } else {
-      codes[0] = __ldg(codes_in);
-      bytes = __ldg(scales_in);
+      codes[0] = *codes_in;
+      bytes = *scales_in;
     }
   }
   char* dst = static_cast<char*>(at.v ? a.v : a.k);

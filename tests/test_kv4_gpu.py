@@ -517,6 +517,41 @@ def test_a_whole_step_on_a_stream_that_is_not_current():
     assert not vb[1, :, 17:].any()
 
 
+def test_many_steps_without_waiting_for_the_gpu():
+    """Steps enqueued one after another, each reading what the one before it and the torch operations between them wrote:
+    the rows, the lengths (advanced on the device) and the queries, all in buffers that are used again."""
+    rng = np.random.default_rng(33)
+    N, Hq, H, E, steps = 2, 4, 2, 64, 60
+    start = [100, 3]
+    cpu, kh, vh = ku.random_cache(rng, N, H, 176, E, E)
+    cache = to_gpu(cpu)
+    qs = ku.bf16(rng.standard_normal((steps, N, Hq, 1, E)))
+    ks, vs = ku.random_rows(rng, (steps, N, H, 1, E)), ku.random_rows(rng, (steps, N, H, 1, E))
+    qg, kg, vg = qs.cuda(), ks.cuda(), vs.cuda()
+    q, k, v, lens, pos = torch.empty_like(qg[0]), torch.empty_like(kg[0]), torch.empty_like(vg[0]), ints(start), ints(start)
+    outs, backs = [], []
+    torch.cuda.synchronize()
+    for i in range(steps):
+        q.copy_(qg[i])
+        k.copy_(kg[i])
+        v.copy_(vg[i])
+        attn.attn_kv4_write(cache, k, v, pos=pos)
+        lens.add_(1)
+        outs.append(attn.attn_decode_kv4(q, cache, scale=0.125, length=176, kv_len=lens, mask_kind="causal"))
+        backs.append(attn.attn_kv4_read(cache, 1, pos=pos, kv_len=lens, dtype=torch.float32))
+        pos.add_(1)
+    torch.cuda.synchronize()
+    for i in range(steps):
+        n_now = [s + i + 1 for s in start]
+        new_k, new_v = (orc4.dequantise(*orc4.quantise(ku.f64(x[i]))) for x in (ks, vs))
+        for n in range(N):
+            kh[n, :, n_now[n] - 1:n_now[n]], vh[n, :, n_now[n] - 1:n_now[n]] = new_k[n], new_v[n]
+        np.testing.assert_array_equal(ku.f64(backs[i][0]), new_k)
+        np.testing.assert_array_equal(ku.f64(backs[i][1]), new_v)
+        ref = orc4.attention(ku.f64(qs[i]), kh, vh, n_now, scale=0.125)
+        ku.compare(*outs[i], *ref, v_most=float(np.abs(vh).max()), scale_of_logits=16.0, what=f"step {i}")
+
+
 def test_a_query_row_that_is_not_finite():
     """Only its own row is lost."""
     rng = np.random.default_rng(32)
