@@ -252,7 +252,8 @@ int attn_decode_indexed(const void* q, const void* k, const void* v, void* out, 
  *        left by 7 is its fp16 pattern.  It is the scale nearest to max|x| / 6
  *        (ties to even), at most 10240 (byte 226).
  *   c_i  4 bits, a sign and one of 0, .5, 1, 1.5, 2, 3, 4, 6 (code 0 to 7): the
- *        nearest to x_i / s (ties to the even code), at most 6; 0 where s = 0.
+ *        nearest to x_i / s (ties to the even code), at most 6; 0 where s = 0 (a
+ *        zero may carry either sign).
  *        Element 2i of a row is the low half of byte i.
  * Values beyond +-61440, infinities among them, are held as +-61440; a block with a
  * NaN has the scale byte 255 and reads back as 16 NaN.  Every c_i * s is exact in
@@ -280,7 +281,9 @@ int attn_decode_indexed(const void* q, const void* k, const void* v, void* out, 
  *           outputs can go to attn_fwd_padded with kv_end
  *
  * Both validate first and launch nothing on error, need no workspace, and return
- * without a host synchronisation.  Errors: ATTN_ERR_NULL_POINTER,
+ * without a host synchronisation.  They and attn_decode_kv4 may start while the
+ * stream's previous kernel is still running (programmatic dependent launch); they
+ * read and write no memory before it is complete.  Errors: ATTN_ERR_NULL_POINTER,
  * ATTN_ERR_BAD_SHAPE (a size < 1, or N*H*L (N*H*rows) or N*H >= 2^31),
  * ATTN_ERR_HEAD_DIM (E or Ev not in {64, 128}), ATTN_ERR_CAPACITY (C not a positive
  * multiple of 16), ATTN_ERR_DTYPE, ATTN_ERR_ALIGNMENT (tensors, cache and strides 16
@@ -315,7 +318,8 @@ int attn_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes
  * holds (blocks with a NaN among them).  A row that sees no key gets out = 0 and
  * lse = -inf (lse = s with a sink).  The call must be decode-shaped,
  * (Hq/H)*L <= 16, else ATTN_ERR_NOT_DECODE: for longer query blocks read the rows
- * back (attn_kv4_read) and use attn_fwd.  Other errors: attn_fwd's codes,
+ * back (attn_kv4_read) and use attn_fwd.  Other errors: attn_fwd's codes
+ * (ATTN_ERR_BAD_SHAPE also for C > 2^31 - 256, or N*H*(C/128 + 2) >= 2^31),
  * ATTN_ERR_KEEP, ATTN_ERR_CAPACITY, ATTN_ERR_WORKSPACE_SIZE.  Nothing is allocated
  * and the host is not synchronised.
  */
