@@ -38,8 +38,8 @@
 // alone is finished by the first of the two, whose part comes last, without writing that.  The
 // counter wraps to zero with the last count (atomicInc), so no launch has to clear it.
 //
-// Measured (one B200, device time): 16 x 131072 x 8 heads of 128 + 128 in 390 to 430 us (2.42 GB,
-// 5.6 to 6.2 TB/s of 6.47 measured copy; 473 us back to back, under the power cap); 32 sequences of
+// Measured (one B200, device time): 16 x 131072 x 8 heads of 128 + 128 in 387 to 445 us (2.42 GB,
+// 5.4 to 6.3 TB/s of 6.47 measured copy; 464 to 471 us back to back, under the power cap); 32 sequences of
 // up to 4096 rows, 8 heads, 27 us; one of 130 rows 6 us.
 
 #include <atomic>
