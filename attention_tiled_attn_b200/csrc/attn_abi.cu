@@ -371,8 +371,9 @@ int attn_decode_kv4(const void* q, const void* k_codes, const void* k_scales, co
   int st = validate(q, k_codes, v_codes, out, lse, N, Hq, H, L, S, E, Ev, scale, mode, sink_logits, nullptr, ATTN_BF16);
   if (st != ATTN_OK) return st;
   if (C < 1 || C % 16 != 0 || S > C) return ATTN_ERR_CAPACITY;
-  // the kernel numbers 128-key chunks (one more per unit) and key positions in 32 bits
-  if (static_cast<long long>(N) * H * ((C - 1) / 128 + 2) >= (1LL << 31) || C > (1LL << 31) - 256) return ATTN_ERR_BAD_SHAPE;
+  // the kernel numbers its work (a unit's 128-key chunks and KV4_UNIT_COST more) and key positions in 32 bits
+  if (static_cast<long long>(N) * H * ((C - 1) / 128 + 1 + KV4_UNIT_COST) >= (1LL << 31) || C > (1LL << 31) - 256)
+    return ATTN_ERR_BAD_SHAPE;
   if (!aligned(k_scales, 16) || !aligned(v_scales, 16) || !aligned(workspace, 16) || (kv_len && !aligned(kv_len, 4)))
     return ATTN_ERR_ALIGNMENT;
   if (static_cast<long long>(Hq / H) * L > 16) return ATTN_ERR_NOT_DECODE;

@@ -64,9 +64,7 @@ constexpr int NPROD = 2;        // producer warps (one thread each)
 constexpr int NMERGE = 2;       // merging warps
 constexpr int NQ = 4;           // units whose query rows may be on chip
 constexpr int MAX_CTAS = 160;   // grid limit, which sizes the workspace
-// What a unit costs besides its chunks, in chunks, when the work is split: 32 ragged sequences of up to 4096 rows take
-// 28 us with 4, 32 with 2, 37 with 1; 5 and 6 change nothing more.
-constexpr int UNIT_COST = 4;
+constexpr int UNIT_COST = KV4_UNIT_COST;
 // A CTA's share, at least (chunks and unit costs): one sequence of 2000 rows takes 12.2 us with 4, 13.0 with 6, 18 with
 // 12; 3 changes nothing more.
 constexpr int MIN_SHARE = 4;

@@ -319,7 +319,7 @@ int attn_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes
  * lse = -inf (lse = s with a sink).  The call must be decode-shaped,
  * (Hq/H)*L <= 16, else ATTN_ERR_NOT_DECODE: for longer query blocks read the rows
  * back (attn_kv4_read) and use attn_fwd.  Other errors: attn_fwd's codes
- * (ATTN_ERR_BAD_SHAPE also for C > 2^31 - 256, or N*H*(C/128 + 2) >= 2^31),
+ * (ATTN_ERR_BAD_SHAPE also for C > 2^31 - 256, or N*H*((C-1)/128 + 5) >= 2^31),
  * ATTN_ERR_KEEP, ATTN_ERR_CAPACITY, ATTN_ERR_WORKSPACE_SIZE.  Nothing is allocated
  * and the host is not synchronised.
  */

@@ -142,6 +142,12 @@ def test_decode_refusals(lib, kw, status):
     assert call_decode(**kw) == status
 
 
+@pytest.mark.parametrize("N", [(1 << 30) - 1, 1 << 29])
+def test_decode_refuses_more_small_sequences_than_it_numbers(lib, N):
+    # a sequence of one chunk takes 5 positions of the 32-bit work list
+    assert call_decode(N=N, Hq=1, S=16, C=16) == -2
+
+
 def test_status_texts(lib):
     for st in (-19, -20):
         assert attn.status_string(st) != "unknown status"
