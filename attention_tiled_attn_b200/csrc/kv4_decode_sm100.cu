@@ -300,6 +300,12 @@ __device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[BYT
   }
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ void merge_bar() { asm volatile("bar.sync 1, %0;" ::"n"(NMERGE * 32) : "memory"); }
 
 // Row r's share of the output: acc * 2^(M) scaled by the merged sum, the sink in the denominator only.
@@ -664,9 +670,9 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
       for (int e = 0; e < 2; ++e) qi[t][e] = (2 * c4 + e + 8 * t) % p.L;
     uint32_t qf[NT][KS][2];
     float o[NT][MD][4];
-    // of the rows 2 c4, 2 c4 + 1: the logits' factor, P_SHIFT - running maximum (base 2), the raw logit above which
-    // the maximum moves (-inf while there is none), the sum
-    float cq[NT][2], bias[NT][2], limit[NT][2], l_run[NT][2];
+    // of the rows 2 c4, 2 c4 + 1: the logits' factor, the running maximum of the raw logits (0 while there is none), the
+    // raw logit above which it moves (-inf while there is none), the sum
+    float cq[NT][2], top[NT][2], limit[NT][2], l_run[NT][2];
     bool ok = true;
     unsigned idx = grp, s = grp, phase = 0;  // the group's next chunk, its stage (idx % NSTAGE) and the stage's parity
     const uint8_t* kp = smem + (j0 + kap_k) * (E / 2) + c4 * KB;  // this lane's bytes in stage 0
@@ -711,7 +717,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
           const float c = fminf(fmaxf(p.c_dot * down, 1e-37f), 3e38f);
           cq[t][0] = __shfl_sync(0xffffffffu, c, 8 * c4);
           cq[t][1] = __shfl_sync(0xffffffffu, c, 8 * c4 + 4);
-          bias[t][0] = bias[t][1] = P_SHIFT;
+          top[t][0] = top[t][1] = 0.f;
           limit[t][0] = limit[t][1] = -INFINITY;
           l_run[t][0] = l_run[t][1] = 0.f;
 #pragma unroll
@@ -858,7 +864,9 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
           };
           if constexpr (NT == 1) load_v(0);
           // online softmax over the tiles' keys.  The running maximum moves only when some logit exceeds it by more
-          // than RESCALE, which one vote of the warp decides; only then the lanes' maxima are reduced.
+          // than RESCALE, which one vote of the warp decides; only then the lanes' maxima are reduced.  The maximum is
+          // subtracted before the factor: the difference is exact where it is small, while a product with the factor is
+          // rounded by more than p can be shifted once the logits pass 2^24 RESCALE.
           float mx[NT][2];
           bool over = false;
 #pragma unroll
@@ -881,15 +889,16 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                 if (m > limit[t][e]) {
                   const float c = RBF ? 1.f : cq[t][e];
-                  const float f = limit[t][e] == -INFINITY ? 0.f : ex2(P_SHIFT - bias[t][e] - m * c);
+                  const float f = limit[t][e] == -INFINITY ? 0.f : ex2((top[t][e] - m) * c);
                   l_run[t][e] *= f;
 #pragma unroll
                   for (int d = 0; d < MD; ++d) {
                     o[t][d][e] *= f;
                     o[t][d][e + 2] *= f;
                   }
-                  bias[t][e] = P_SHIFT - m * c;
-                  limit[t][e] = m + RESCALE / c;
+                  top[t][e] = m;
+                  // rounded down (an approximate reciprocal is off by 2^-23): no p is above 2^(P_SHIFT + RESCALE)
+                  limit[t][e] = __fadd_rd(m, RESCALE * (1.f - 0x1p-20f) * (RBF ? 1.f : rcp_approx(c)));
                 }
               }
           }
@@ -899,9 +908,11 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
             const float c0 = RBF ? 1.f : cq[t][0], c1 = RBF ? 1.f : cq[t][1];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              float x0, x1, x2, x3;
-              fma2g(x0, x1, sc[mt][t][0], sc[mt][t][1], c0, c1, bias[t][0], bias[t][1]);
-              fma2g(x2, x3, sc[mt][t][2], sc[mt][t][3], c0, c1, bias[t][0], bias[t][1]);
+              float x0 = sc[mt][t][0], x1 = sc[mt][t][1], x2 = sc[mt][t][2], x3 = sc[mt][t][3];
+              add2(x0, x1, -top[t][0], -top[t][1]);
+              add2(x2, x3, -top[t][0], -top[t][1]);
+              fma2g(x0, x1, x0, x1, c0, c1, P_SHIFT, P_SHIFT);
+              fma2g(x2, x3, x2, x3, c0, c1, P_SHIFT, P_SHIFT);
               const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
               add2(l_run[t][0], l_run[t][1], p0, p1);
               add2(l_run[t][0], l_run[t][1], p2, p3);
@@ -954,7 +965,9 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
             l += __shfl_xor_sync(0xffffffffu, l, 4);
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
-            if (ra == 0) my_ml[8 * t + e] = make_float2(limit[t][e] == -INFINITY ? -INFINITY : P_SHIFT - bias[t][e], l);
+            // a maximum past fp32 is a NaN and not -inf, which stands for no key
+            const float m = top[t][e] * (RBF ? 1.f : cq[t][e]);
+            if (ra == 0) my_ml[8 * t + e] = make_float2(limit[t][e] == -INFINITY ? -INFINITY : m - m == 0.f ? m : __int_as_float(0x7fffffff), l);
           }
 #pragma unroll
           for (int d = 0; d < MD; ++d)
