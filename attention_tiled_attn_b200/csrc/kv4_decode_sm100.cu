@@ -35,7 +35,9 @@
 //
 // A unit inside one CTA is finished there.  Otherwise each CTA writes its (m, l, O) and counts it;
 // the CTA whose count completes the unit merges them at its end.  A unit shared with the next CTA
-// alone is finished by the first of the two, whose part comes last, without writing that.  The
+// alone is finished by the first of the two, without writing its part, if the other's is there by
+// then.  Whichever does it, each part is summed by itself and the parts are joined in the order of
+// their keys by the same operations (join_rows, join_sums), so that equal calls give equal bits.  The
 // counter wraps to zero with the last count (atomicInc), so no launch has to clear it.
 //
 // Measured (one B200, device time): 16 x 131072 x 8 heads of 128 + 128 in 387 to 445 us (2.42 GB,
@@ -117,8 +119,8 @@ struct Cfg {
   static constexpr int OFF_Q = OFF_MERGE + NBUF * NCW * NX * 16;  // [NQ][8 NT][E] bf16
   static constexpr int OFF_ML = OFF_Q + NQ * Q_SLOT;              // [NBUF][NCW][8 NT] float2
   static constexpr int OFF_WT = OFF_ML + NBUF * NCW * 8 * NT * 8; // [NCW][8 NT] float: weights of the warps' states
-  static constexpr int OFF_OWT = OFF_WT + NCW * 8 * NT * 4;       // [8 NT] float: weights of the next CTA's partial
-  static constexpr int OFF_BAR = OFF_OWT + 8 * NT * 4;
+  static constexpr int OFF_JOIN = OFF_WT + NCW * 8 * NT * 4;      // [8 NT] float4: a row's factors where two parts are joined
+  static constexpr int OFF_BAR = OFF_JOIN + 8 * NT * 16;
   static constexpr int NBAR = 2 * NSTAGE + 2 * NQ + 2 * NBUF;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;             // Misc
   static constexpr int SMEM = OFF_MISC + 128;
@@ -308,17 +310,47 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 __device__ __forceinline__ void merge_bar() { asm volatile("bar.sync 1, %0;" ::"n"(NMERGE * 32) : "memory"); }
 
+// a query head's sink logit in base 2
+__device__ __forceinline__ float sink2(const Params& p, int head) {
+  return p.sink ? __fmul_rn(p.sink[head], LOG2E) : -INFINITY;
+}
+
 // Row r's share of the output: acc * 2^(M) scaled by the merged sum, the sink in the denominator only.
-// Returns the factor for acc, and the row's lse in *lse.
+// Returns the factor for acc, and the row's lse in *lse.  (It is used in several places, which must not
+// differ in what the compiler fuses.)
 __device__ __forceinline__ float row_factor(float M, float l, float s2, float* lse) {
   const float m = fmaxf(M, s2);
   float f = 1.f;
   if (m != -INFINITY) {
-    f = M == -INFINITY ? 0.f : ex2(M - m);
-    l = l * f + 128.f * ex2(s2 - m);  // 128 = 2^P_SHIFT
+    f = M == -INFINITY ? 0.f : ex2(__fsub_rn(M, m));
+    l = fmaf(l, f, 128.f * ex2(__fsub_rn(s2, m)));  // 128 = 2^P_SHIFT
   }
-  *lse = l == 0.f ? -INFINITY : (m + log2f(l) - P_SHIFT) * LN2;
-  return l == 0.f ? 0.f : f / l;
+  *lse = l == 0.f ? -INFINITY : __fmul_rn(__fsub_rn(__fadd_rn(m, log2f(l)), P_SHIFT), LN2);
+  return l == 0.f ? 0.f : __fdiv_rn(f, l);
+}
+
+// Joins up to FEW parts of a row, (m, l) each in the order of their keys ((-inf, 0): none): f[y] becomes part y's factor
+// in the sums; the row's share of the output is the joined sums times the returned factor.
+__device__ __forceinline__ float join_rows(const float2 (&ml)[FEW], float s2, float (&f)[FEW], float* lse) {
+  float M = ml[0].x, l = 0.f;
+#pragma unroll
+  for (int y = 1; y < FEW; ++y) M = fmaxf(M, ml[y].x);
+#pragma unroll
+  for (int y = 0; y < FEW; ++y) {
+    f[y] = ml[y].x == -INFINITY ? 0.f : ex2(__fsub_rn(ml[y].x, M));
+    l = fmaf(ml[y].y, f[y], l);
+  }
+  return row_factor(M, l, s2, lse);
+}
+
+// The joined sums of two rows (x and z, y and w), times their factors.
+__device__ __forceinline__ float4 join_sums(const float4 (&v)[FEW], const float (&f0)[FEW], const float (&f1)[FEW], float all0,
+                                            float all1) {
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int y = 0; y < FEW; ++y)
+    acc = make_float4(fmaf(v[y].x, f0[y], acc.x), fmaf(v[y].y, f1[y], acc.y), fmaf(v[y].z, f0[y], acc.z), fmaf(v[y].w, f1[y], acc.w));
+  return make_float4(__fmul_rn(acc.x, all0), __fmul_rn(acc.y, all1), __fmul_rn(acc.z, all0), __fmul_rn(acc.w, all1));
 }
 
 // Writes float4 x of a unit's O^T: rows 2 (x % 4) and + 1 of its row block, two dimensions.
@@ -345,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
   float4* merge = reinterpret_cast<float4*>(smem + C::OFF_MERGE);
   float2* merge_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
   float* wts = reinterpret_cast<float*>(smem + C::OFF_WT);
-  float* other_wts = reinterpret_cast<float*>(smem + C::OFF_OWT);
+  float4* join = reinterpret_cast<float4*>(smem + C::OFF_JOIN);
   auto full_bar = [&](unsigned s) -> uint32_t { return sb + C::OFF_BAR + 8u * s; };
   auto empty_bar = [&](unsigned s) -> uint32_t { return sb + C::OFF_BAR + 8u * (C::NSTAGE + s); };
   auto qfull_bar = [&](unsigned k) -> uint32_t { return sb + C::OFF_BAR + 8u * (2 * C::NSTAGE + k % NQ); };
@@ -526,24 +558,22 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
         }
 #pragma unroll
         for (int y = 0; y < NCW; ++y) l = fmaf(e[y].y, e[y].x == -INFINITY ? 0.f : ex2(e[y].x - M), l);
-        if (__builtin_expect(there, 0)) {  // r is the row of other_ml too: the stride of z is a multiple of 8 NT
-          const float own = M;
-          M = fmaxf(M, other_ml.x);
-          l = l * (own == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(own - M)) +
-              other_ml.y * (other_ml.x == -INFINITY ? (other_ml.y == 0.f ? 0.f : 1.f) : ex2(other_ml.x - M));
-        }
         const float m = buf_ml[me * 8 * NT + r].x;
         float wt = m == -INFINITY ? 0.f : ex2(m - M);
-        if (whole || there) {
+        if (whole) {
           float lse;
-          const float f = row_factor(M, l, p.sink ? p.sink[w.h * p.group + r / p.L] * LOG2E : -INFINITY, &lse);
-          wt *= f;
-          if (me == w0) {
-            if (p.lse) p.lse[w.unit(p) * p.R + r] = lse;
-            if (there) other_wts[r] = other_ml.x == -INFINITY ? 0.f : ex2(other_ml.x - M) * f;
-          }
+          wt *= row_factor(M, l, sink2(p, w.h * p.group + r / p.L), &lse);
+          if (me == w0 && p.lse) p.lse[w.unit(p) * p.R + r] = lse;
         } else if (me == w0) {
-          reinterpret_cast<float2*>(mine + MAX_ROWS * 128)[r] = make_float2(M, l);
+          if (__builtin_expect(there, 0)) {  // r is the row of other_ml too: the stride of z is a multiple of 8 NT
+            const float2 ml[FEW] = {make_float2(M, l), other_ml, make_float2(-INFINITY, 0.f), make_float2(-INFINITY, 0.f)};
+            float f[FEW], lse;
+            const float all = join_rows(ml, sink2(p, w.h * p.group + r / p.L), f, &lse);
+            join[r] = make_float4(f[0], f[1], all, 0.f);
+            if (p.lse) p.lse[w.unit(p) * p.R + r] = lse;
+          } else {
+            reinterpret_cast<float2*>(mine + MAX_ROWS * 128)[r] = make_float2(M, l);
+          }
         }
         wts[me * 8 * NT + r] = wt;
       }
@@ -553,16 +583,11 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
         const int r = 8 * t + 2 * (mt & 3);
         if (r >= p.R) continue;
         constexpr int PER = MD * 32 / (NMERGE * 32);  // float4 of a thread per row block
-        float4 acc[PER];
+        float4 acc[PER], next[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (__builtin_expect(there, 0)) {
-          const float f0 = other_wts[r], f1 = r + 1 < p.R ? other_wts[r + 1] : 0.f;
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(other) + t * MD * 32 + i * NMERGE * 32 + mt);
-            acc[i] = make_float4(v.x * f0, v.y * f1, v.z * f0, v.w * f1);
-          }
+        for (int i = 0; i < PER; ++i) {
+          acc[i] = next[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (__builtin_expect(there, 0)) next[i] = __ldcg(reinterpret_cast<const float4*>(other) + t * MD * 32 + i * NMERGE * 32 + mt);
         }
         for (int y0 = 0; y0 < na; y0 += GW) {
 #pragma unroll
@@ -577,6 +602,16 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
               acc[i].z = fmaf(v.z, f0, acc[i].z);
               acc[i].w = fmaf(v.w, f1, acc[i].w);
             }
+          }
+        }
+        if (__builtin_expect(there, 0)) {
+          const float4 j0 = join[r], j1 = r + 1 < p.R ? join[r + 1] : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float f0[FEW] = {j0.x, j0.y, 0.f, 0.f}, f1[FEW] = {j1.x, j1.y, 0.f, 0.f};
+          const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const float4 v[FEW] = {acc[i], next[i], none, none};
+            acc[i] = join_sums(v, f0, f1, j0.z, j1.z);
           }
         }
 #pragma unroll
@@ -997,32 +1032,20 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
         const int r = 8 * (x / (32 * MD)) + 2 * (x & 3);
         if (r >= p.R) continue;
         float4 v[FEW];
-        float4 e[FEW];  // (m, l) of rows r and r + 1
+        float2 e0[FEW], e1[FEW];  // (m, l) of rows r and r + 1
 #pragma unroll
         for (int y = 0; y < FEW; ++y) {
           const float* src = slot(y < nseg ? y : 0);
           v[y] = __ldcg(reinterpret_cast<const float4*>(src) + x);
-          e[y] = __ldcg(reinterpret_cast<const float4*>(src + MAX_ROWS * 128 + 2 * r));
-          if (y >= nseg) e[y] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f), v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 e = __ldcg(reinterpret_cast<const float4*>(src + MAX_ROWS * 128 + 2 * r));
+          e0[y] = make_float2(e.x, e.y);
+          e1[y] = make_float2(e.z, e.w);
+          if (y >= nseg) e0[y] = e1[y] = make_float2(-INFINITY, 0.f), v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        float M0 = e[0].x, M1 = e[0].z, l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int y = 1; y < FEW; ++y) {
-          M0 = fmaxf(M0, e[y].x);
-          M1 = fmaxf(M1, e[y].z);
-        }
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int y = 0; y < FEW; ++y) {
-          const float f0 = e[y].x == -INFINITY ? 0.f : ex2(e[y].x - M0), f1 = e[y].z == -INFINITY ? 0.f : ex2(e[y].z - M1);
-          l0 = fmaf(e[y].y, f0, l0);
-          l1 = fmaf(e[y].w, f1, l1);
-          acc = make_float4(fmaf(v[y].x, f0, acc.x), fmaf(v[y].y, f1, acc.y), fmaf(v[y].z, f0, acc.z), fmaf(v[y].w, f1, acc.w));
-        }
-        float lse0, lse1;
-        const float f0 = row_factor(M0, l0, p.sink ? p.sink[h * p.group + r / p.L] * LOG2E : -INFINITY, &lse0);
-        const float f1 = r + 1 < p.R ? row_factor(M1, l1, p.sink ? p.sink[h * p.group + (r + 1) / p.L] * LOG2E : -INFINITY, &lse1) : 0.f;
-        store_out<EV, MD>(p, unit, x, make_float4(acc.x * f0, acc.y * f1, acc.z * f0, acc.w * f1));
+        float f0[FEW], f1[FEW], lse0, lse1;
+        const float all0 = join_rows(e0, sink2(p, h * p.group + r / p.L), f0, &lse0);
+        const float all1 = join_rows(e1, r + 1 < p.R ? sink2(p, h * p.group + (r + 1) / p.L) : -INFINITY, f1, &lse1);
+        store_out<EV, MD>(p, unit, x, join_sums(v, f0, f1, all0, all1));
         if ((x & 28) == 0 && (x >> 5) % MD == 0 && p.lse) {
           p.lse[static_cast<size_t>(unit) * p.R + r] = lse0;
           if (r + 1 < p.R) p.lse[static_cast<size_t>(unit) * p.R + r + 1] = lse1;
@@ -1050,7 +1073,7 @@ __global__ void __launch_bounds__(Cfg<E, EV, NT>::THREADS, 1) kv4_decode_kernel(
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
       float lse;
-      const float f = row_factor(M, l, p.sink ? p.sink[h * p.group + r / p.L] * LOG2E : -INFINITY, &lse);
+      const float f = row_factor(M, l, sink2(p, h * p.group + r / p.L), &lse);
 #pragma unroll
       for (int i = 0; i < (MAX_CTAS + 31) / 32; ++i)
         if (32 * i + lane < nseg) seg_wts[(32 * i + lane) * 8 * NT + r] = e[i].x * f;

@@ -316,6 +316,8 @@ int attn_kv4_read(const void* k_codes, const void* k_scales, const void* v_codes
  *           their own may overlap, captured or not.
  * Logits are held in fp32: finite ones of any size give a softmax, a row whose
  * logits pass fp32's range gives NaN.
+ * The same call on the same kind of device gives the same bits, whatever else the
+ * device is doing.
  * A key that the masks hide from a row takes no part in it, whatever the cache
  * holds (blocks with a NaN among them).  A row that sees no key gets out = 0 and
  * lse = -inf (lse = s with a sink).  The call must be decode-shaped,
