@@ -59,6 +59,8 @@ __device__ __forceinline__ uint32_t kv4_scale2(uint32_t byte) { return byte * 0x
 __device__ __forceinline__ void overlap_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void overlap_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The launch's own status.  A failure is taken back from the runtime, so that no later call takes it for its own; an error
+// that another call left there is not looked at.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_overlapped(void (*kern)(KArgs...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
                               Args... args) {
@@ -72,7 +74,9 @@ cudaError_t launch_overlapped(void (*kern)(KArgs...), unsigned grid, unsigned th
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {

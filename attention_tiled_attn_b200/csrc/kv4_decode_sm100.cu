@@ -1129,11 +1129,13 @@ int launch_impl(const Params& p, unsigned G, cudaStream_t stream) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -13;
   for (int attempt = 0; attempt < 2; ++attempt) {
     if (!raised[dev].load(std::memory_order_acquire)) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) break;
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) {
+        cudaGetLastError();
+        break;
+      }
       raised[dev].store(true, std::memory_order_release);
     }
     if (launch_overlapped(kern, G, C::THREADS, C::SMEM, stream, p, G) == cudaSuccess) return 0;
-    cudaGetLastError();
     raised[dev].store(false, std::memory_order_release);
   }
   return -13;

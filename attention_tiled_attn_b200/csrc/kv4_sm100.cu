@@ -324,14 +324,14 @@ int launch_kv4_write(const Kv4WriteArgs& a, bool bf16, int num_sms, cudaStream_t
   const cudaError_t e = !bf16                                           ? write_rows<false, WIDE<false>>(a, stream)
                         : many(a.N, a.H, a.L, a.E, a.Ev, num_sms) ? write_rows<true, WIDE<true>>(a, stream)
                                                                         : write_rows<true, 1>(a, stream);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 0 : -13;
+  return e == cudaSuccess ? 0 : -13;
 }
 
 int launch_kv4_read(const Kv4ReadArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
   const cudaError_t e = !bf16                                              ? read_rows<false, WIDE<false>>(a, stream)
                         : many(a.N, a.H, a.rows, a.E, a.Ev, num_sms) ? read_rows<true, WIDE<true>>(a, stream)
                                                                            : read_rows<true, 1>(a, stream);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 0 : -13;
+  return e == cudaSuccess ? 0 : -13;
 }
 
 }  // namespace attn
