@@ -383,6 +383,8 @@ def _cache_shape(cache):
             and kc.dtype is ks.dtype is vc.dtype is vs.dtype is torch.uint8
             and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and vs.is_contiguous()):
         raise ValueError("the cache must be contiguous uint8 CUDA tensors on one device")
+    if max(N, H, C, 2 * half, 2 * half_v) >= 2**31:  # the C interface's sizes; see _int32
+        raise ValueError("the cache's sizes must fit in 32 bits")
     return N, H, C, 2 * half, 2 * half_v, dev
 
 
@@ -479,7 +481,7 @@ def attn_kv4_write(cache, k: torch.Tensor, v: torch.Tensor, *, start: int = 0, p
         raise ValueError("the last dimension of k and v must be contiguous")
     _check_index("pos", pos, N, dev)
     _check_index("count", count, N, dev)
-    _int32(start=start)
+    _int32(start=start, rows=ks[2])
     kc, ksc, vc, vsc = cache
     args = (k.data_ptr(), v.data_ptr(), kc.data_ptr(), ksc.data_ptr(), vc.data_ptr(), vsc.data_ptr(), N, H, ks[2], C, E, Ev,
             kst[0], kst[1], kst[2], vst[0], vst[1], vst[2], start, _address(pos), _address(count), DTYPES[k.dtype])
