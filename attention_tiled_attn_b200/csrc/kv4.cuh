@@ -5,7 +5,9 @@
 //   s  5 exponent bits (bias 15) and 3 mantissa bits, no sign: the byte shifted left
 //      by 7 is the same value's fp16 pattern.  0 .. 226 are written (226 is 10240, so
 //      6 * s stays below fp16's largest value); 255 (an fp16 NaN) marks a block that
-//      had a NaN.
+//      had a NaN.  227 .. 254 are outside the format: as fp16 patterns they are numbers, of
+//      which 6 s overflows, infinities and NaN, and where a mask cuts a chunk the decode takes
+//      them all for NaN, so that they cannot reach a row that does not see their key.
 //   c  a sign bit and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (e2m1); element 2i of a row is
 //      the low half of byte i.
 // A product c * s has at most 2 + 4 significant bits and is a multiple of 2^-18 below

@@ -257,7 +257,10 @@ int attn_decode_indexed(const void* q, const void* k, const void* v, void* out, 
  *        Element 2i of a row is the low half of byte i.
  * Values beyond +-61440, infinities among them, are held as +-61440; a block with a
  * NaN has the scale byte 255 and reads back as 16 NaN.  Every c_i * s is exact in
- * fp16, bf16 and fp32.
+ * fp16, bf16 and fp32.  The scale bytes 227 to 254 are not part of the format:
+ * attn_kv4_write never stores them, and what a block with one stands for is not
+ * defined (a number, an infinity or a NaN, not the same in every call).  Rows that
+ * are not asked for and keys that the masks hide may hold any bytes.
  *
  * attn_kv4_write -- rounds new rows and stores them.
  *   k, v    new rows in `dtype` (ATTN_BF16 or ATTN_FP32); value e of row l of
