@@ -31,7 +31,10 @@
 // Q is held in fp16 with each row shifted by a power of two, so that its largest element is in
 // [2^14, 2^15): nothing above 2^-31 of it is lost.  P is rounded to fp16 times 2^7 (p is at most
 // 2^8 before that, see RESCALE): 11 bits down to 2^-21 of the running maximum's probability, an
-// absolute 2^-32 below.  Sums, maxima and outputs are fp32.
+// absolute 2^-32 below.  The product with V takes 16-bit operands; against a P in fp32 this moves
+// 7 to 10% of the bf16 outputs, most of them to the next value (6e-4 to 1e-3 of the outputs' norm),
+// and the error against 64 bits stays the output rounding's (1.6e-3 in either form).  Sums, maxima
+// and outputs are fp32.
 //
 // A unit inside one CTA is finished there.  Otherwise each CTA writes its (m, l, O) and counts it;
 // the CTA whose count completes the unit merges them at its end.  A unit shared with the next CTA
@@ -40,9 +43,9 @@
 // their keys by the same operations (join_rows, join_sums), so that equal calls give equal bits.  The
 // counter wraps to zero with the last count (atomicInc), so no launch has to clear it.
 //
-// Measured (one B200, device time): 16 x 131072 x 8 heads of 128 + 128 in 387 to 445 us (2.42 GB,
-// 5.4 to 6.3 TB/s of 6.47 measured copy; 464 to 471 us back to back, under the power cap); 32 sequences of
-// up to 4096 rows, 8 heads, 27 us; one of 130 rows 6 us.
+// Measured (one B200, device time): 16 x 131072 x 8 heads of 128 + 128 in 385 to 440 us (2.42 GB,
+// 5.5 to 6.3 TB/s of 6.47 measured copy; 438 us and more back to back, under the power cap); 32 sequences of
+// up to 4096 rows, 8 heads, 29 us; one of 130 rows 6.1 us.
 
 #include <atomic>
 #include <cstdint>
@@ -67,11 +70,13 @@ constexpr int NMERGE = 2;       // merging warps
 constexpr int NQ = 4;           // units whose query rows may be on chip
 constexpr int MAX_CTAS = 160;   // grid limit, which sizes the workspace
 constexpr int UNIT_COST = KV4_UNIT_COST;
-// A CTA's share, at least (chunks and unit costs): one sequence of 2000 rows takes 12.2 us with 4, 13.0 with 6, 18 with
-// 12; 3 changes nothing more.
+// A CTA's share, at least (chunks and unit costs): one sequence of 2000 rows takes 9.8 us with 4, 10.7 with 3, 10.5 with
+// 6, 13.1 with 12.
 constexpr int MIN_SHARE = 4;
 constexpr int FEW = 4;          // partials of a unit that are merged in one round of loads
-constexpr int NO_SPLIT = 6;     // a unit of so many chunks is never split (3 and 12 measure the same)
+// A unit of so many chunks is never split: 64 sequences of up to 300 rows take 18.5 us with 3, 6 or 12, 19.3 with 0.
+// Longer ragged sequences do not gain: the step of 32 of up to 8000 rows takes 49 us with 6 or 12, 45 with 0 or 3.
+constexpr int NO_SPLIT = 6;
 constexpr float RESCALE = 8.f;  // the running maximum follows the true one within 2^8
 constexpr float P_SHIFT = 7.f;  // P is held times 2^7
 constexpr size_t WS_HEAD = ATTN_DECODE_KV4_WORKSPACE_ZERO;  // arrival counters, one per CTA
@@ -98,9 +103,11 @@ struct Params {
 
 template <int E, int EV, int NT>
 struct Cfg {
-  // A consumer warp works on MT 16-key tiles at once: 64 keys for 8 query rows, 32 for 16 (what 168 registers hold);
-  // the GW warps of a group share a chunk, the NG groups take chunks in turn.  More and narrower warps (12 of 32 keys)
-  // measured slower (16 x 131072 x 8 heads: 460 us against 421): a warp's fixed work per chunk is what they repeat.
+  // A consumer warp works on MT 16-key tiles at once: 64 keys for 8 query rows, 32 for 16.  Every warp has 168 registers:
+  // 8 rows fit them; of the 16-row forms 64 + 64 and 128 + 64 rbf do too, the others spill (128 + 64 dot 16 bytes, 64 +
+  // 128 20 and 32, 128 + 128 64 and 152).  The GW warps of a group share a chunk, the NG groups take chunks in turn.
+  // More and narrower warps (12 of 32 keys) measured slower (16 x 131072 x 8 heads: 460 us against 421): a warp's fixed
+  // work per chunk is what they repeat.
   static constexpr int MT = 4 / NT, GW = KC / (16 * MT), NG = CONSUMERS / GW;
   static constexpr int NCW = CONSUMERS;
   static constexpr int WARPS = NCW + NPROD + NMERGE;

@@ -15,7 +15,7 @@
 // Both passes move every byte once: (E + Ev) values in (out) and 9/16 of a byte per value out
 // (in), so HBM bounds them.  A thread works on blocks of 16 values: 32 (bf16) or 64 (fp32)
 // bytes of values in 32-byte accesses, 8 bytes of elements and one scale byte, neighbouring
-// threads on neighbouring blocks, so that every 32-byte sector is moved whole.  It has BPT
+// threads on neighbouring blocks, so that every 32-byte sector is moved whole.  It has PER
 // blocks in flight, and a CTA finds its place in the tensors once.
 
 #include <cstdint>
@@ -56,8 +56,9 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 }
 
 // Blocks of 16 per thread.  64 bytes of values in flight per thread and small CTAs measured best: bf16 2 blocks (4 x
-// 8192 x 8 rows of 128 + 128 written in 32 us; 1 block 37, 4 blocks of 256 threads 40; 131072 x 8 rows read in 103 us,
-// 6.7 TB/s; 1 block 113), fp32 1 block (written in 45 us; 2 blocks 49).  bf16 calls whose tiles of 2 would leave SMs
+// 8192 x 8 rows of 128 + 128 written in 32 us; 1 block 37, 4 blocks of 256 threads 40; 131072 x 8 rows read in 102 us,
+// 6.8 TB/s; 1 block 113), fp32 1 block (4 x 8192 x 8 rows written in 46 us, 6.6 TB/s; 2 blocks 49; 131072 x 8 rows read in
+// 182 us, 6.7 TB/s).  bf16 calls whose tiles of 2 would leave SMs
 // without a CTA take 1.  Writing, the two are WT blocks apart: its loads miss every cache, and a warp's 32-byte pieces
 // then make whole lines (strided sources 32 us against 34).  Reading, they are neighbours, which share their address.
 template <bool BF16>
