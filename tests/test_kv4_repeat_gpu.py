@@ -72,3 +72,43 @@ def test_equal_bits_however_many_sms_are_busy(name):
         if not all(torch.equal(a, b) for a, b in zip(got, want)):
             differ.append(busy)
     assert not differ, f"other bits with {differ} SMs busy"
+
+
+def test_equal_bits_on_many_streams_and_in_graphs():
+    """Calls of different shapes on four streams at once, half of them in replayed graphs: each gives the bits that it
+    gives alone."""
+    calls, want = [], []
+    for i, name in enumerate(CASES):
+        c = CASES[name]
+        g = torch.Generator(device="cuda").manual_seed(50 + i)
+        cache = random_cache(g, c["N"], c["H"], -(-c["S"] // 16) * 16, c["E"], c["Ev"])
+        q = (0.3 * torch.randn(c["N"], c["Hq"], c["L"], c["E"], device="cuda", generator=g)).bfloat16()
+        kv_len = torch.randint(0, c["S"] + 1, (c["N"],), dtype=torch.int32, device="cuda", generator=g)
+        calls.append(lambda q=q, cache=cache, kv_len=kv_len, c=c, **kw: attn.attn_decode_kv4(
+            q, cache, scale=c["E"] ** -0.5, length=c["S"], kv_len=kv_len, mask_kind="causal", **kw))
+        want.append(bits(calls[-1]()))
+    graphs = []
+    for call in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = call()
+        graphs.append((graph, got))
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for turn in range(12):
+        eager = []
+        for i in range(len(calls)):
+            j = (i + turn) % len(calls)  # the call on stream i; the next stream replays the graph of another one
+            if (i + turn // 4) % 2:
+                with torch.cuda.stream(streams[i]):
+                    graphs[j][0].replay()
+            else:
+                eager.append((j, calls[j](stream=streams[i])))
+        torch.cuda.synchronize()
+        for j, got in eager:
+            assert all(torch.equal(a, b) for a, b in zip(bits(got), want[j])), f"turn {turn}, case {j}"
+    for graph, got in graphs:
+        graph.replay()
+    torch.cuda.synchronize()
+    for (_, got), w in zip(graphs, want):
+        assert all(torch.equal(a, b) for a, b in zip(bits(got), w))
